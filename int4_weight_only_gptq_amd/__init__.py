@@ -13,7 +13,7 @@ import os
 
 __all__ = ["load", "lib_path", "QGemmError", "qgemm_int4", "qgemm_int4_noalloc", "qgemm_int4_lora",
            "qgemm_int4_epilogue", "qgemm_int4_dequant", "gemm_dense",
-           "gemm_dense_batched", "describe_int4",
+           "gemm_dense_batched", "gemm_grouped", "describe_int4",
            "workspace_size", "probe_mfma_bf16", "probe_copy", "probe_read",
            "abi_version", "PATHS", "LAYOUTS"]
 
@@ -91,6 +91,8 @@ def load():
     lib.gemm_dense_batched.restype = i32
     lib.gemm_dense_batched.argtypes = [i32, i32, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64,
                                        i64, vp]
+    lib.gemm_grouped.restype = i32
+    lib.gemm_grouped.argtypes = [i32, i32, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp]
     lib.qg_probe_mfma_bf16.restype = i32
     lib.qg_probe_mfma_bf16.argtypes = [i64, i32, vp, vp]
     lib.qg_probe_copy.restype = i32
@@ -409,6 +411,84 @@ def gemm_dense_batched(layout: str, a, b, out=None, stream=None):
                                 b.stride(0), out.data_ptr(), out.stride(1), out.stride(0),
                                 _stream(a, stream))
     _check(st, "gemm_dense_batched")
+    return out
+
+
+def _launch_on(device, stream):
+    """Context of a call: its tensors' device is current, and new tensors are allocated on
+    the launch stream (so that the caching allocator orders their reuse with the call)."""
+    import contextlib
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return torch.cuda.stream(_torch_stream(device, stream))
+
+
+def _same_device(first, *others):
+    if first.device.type != "cuda":
+        raise ValueError("expected tensors on a GPU")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _rows_ld(t, what):
+    """Distance in elements between the rows of a matrix, or of each matrix of a stack."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % what)
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _group_count(offsets):
+    import torch
+
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 vector of groups + 1 entries")
+    return offsets.numel() - 1
+
+
+def gemm_grouped(layout: str, a, b, offsets, out=None, stream=None):
+    """The products of a linear layer grouped by expert: rows offsets[e] .. offsets[e + 1] - 1
+    belong to group e (offsets: int32 [groups + 1] on the device, non-decreasing; see
+    qgemm_grouped.h).  bf16 / fp16 with fp32 accumulation, or fp32 throughout.
+
+    "NT": a [rows][K], b [groups][N][K] -> [rows][N], out[r] = a[r] . b[e]^T
+    "NN": a [rows][K], b [groups][K][N] -> [rows][N], out[r] = a[r] . b[e]
+    "TN": a [rows][M], b [rows][N] -> [groups][M][N], out[e] = a[rows of e]^T . b[rows of e]
+
+    Rows outside every group are left as they were in ``out`` (a new ``out`` is not
+    initialised there).  Nothing is read back to the host."""
+    import torch
+
+    lib = load()
+    dtype = _dtype_of(a, b)
+    groups = _group_count(offsets)
+    if layout == "TN":
+        if a.dim() != 2 or b.dim() != 2 or a.shape[0] != b.shape[0]:
+            raise ValueError("TN: a must be [rows][M] and b [rows][N]")
+        (K, M), N = a.shape, b.shape[1]
+        shape, sb = (groups, M, N), 0
+    elif layout in ("NT", "NN"):
+        M, K = a.shape if a.dim() == 2 else (-1, -1)
+        if b.dim() != 3 or b.shape[0] != groups or b.shape[2 if layout == "NT" else 1] != K:
+            raise ValueError("%s: a must be [rows][K] and b [groups]%s" %
+                             (layout, "[N][K]" if layout == "NT" else "[K][N]"))
+        N = b.shape[1 if layout == "NT" else 2]
+        shape, sb = (M, N), b.stride(0)
+    else:
+        raise ValueError(layout)
+    _same_device(a, b, offsets, out)
+    with _launch_on(a.device, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=a.dtype, device=a.device)
+        elif tuple(out.shape) != shape or out.dtype != a.dtype:
+            raise ValueError("out must be %s of the operands' dtype" % (list(shape),))
+        sc = out.stride(0) if layout == "TN" else 0
+        st = lib.gemm_grouped(LAYOUTS[layout], _DTYPES[dtype], groups, offsets.data_ptr(), M, N, K, a.data_ptr(),
+                              _rows_ld(a, "a"), b.data_ptr(), _rows_ld(b, "b"), sb, out.data_ptr(),
+                              _rows_ld(out, "out"), sc, _stream(a, stream))
+    _check(st, "gemm_grouped")
     return out
 
 

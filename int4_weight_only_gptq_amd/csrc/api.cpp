@@ -1,6 +1,7 @@
 // C ABI of the library: argument validation, path choice and launch.
 // Declarations and the contract of each entry point are in include/qgemm.h.
 #include "qgemm.h"
+#include "qgemm_grouped.h"
 
 #include <hip/hip_runtime.h>
 #include <stdio.h>
@@ -28,6 +29,9 @@ int32_t hip_status(hipError_t e) {
 }
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Sizes of the grouped products: rows and tiles are counted in 32 bits.
+constexpr int64_t kMaxGroupedSize = ((int64_t)1 << 31) - 1024;
 
 // Validation shared by the int4 entry points; returns QG_OK or the error.
 int32_t check_int4(const void* x, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
@@ -411,6 +415,30 @@ int32_t gemm_dense_batched(int32_t layout, int32_t dtype, int64_t batch, int64_t
                            int64_t stride_b, void* C, int64_t ldc, int64_t stride_c, void* stream) {
   return run_dense(layout, dtype, batch, M, N, K, A, lda, stride_a, B, ldb, stride_b, C, ldc, stride_c,
                    stream);
+}
+
+int32_t gemm_grouped(int32_t layout, int32_t dtype, int64_t groups, const int32_t* offsets, int64_t M, int64_t N,
+                     int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b, void* C,
+                     int64_t ldc, int64_t stride_c, void* stream) {
+  if (layout < QG_NT || layout > QG_TN) return QG_ERR_LAYOUT;
+  if (dtype != QG_BF16 && dtype != QG_FP16 && dtype != QG_FP32) return QG_ERR_DTYPE;
+  const uintptr_t esize = dtype == QG_FP32 ? 4 : 2;
+  if (M < 0 || N < 0 || K < 0 || groups < 0 || stride_b < 0 || stride_c < 0) return QG_ERR_SHAPE;
+  if (M > kMaxGroupedSize || N > kMaxGroupedSize || K > kMaxGroupedSize || groups > QG_MAX_GROUPS) return QG_ERR_SHAPE;
+  if (M == 0 || N == 0 || groups == 0) return QG_OK;
+  if (C == nullptr || offsets == nullptr) return QG_ERR_NULL;
+  if (ldc < N) return QG_ERR_SHAPE;
+  if (layout == QG_TN && groups > 1 && stride_c < (M - 1) * ldc + N) return QG_ERR_SHAPE;   // outputs must not overlap
+  if (!aligned(C, esize) || !aligned(offsets, 4)) return QG_ERR_ALIGN;
+  if (K > 0) {
+    if (A == nullptr || B == nullptr) return QG_ERR_NULL;
+    if (lda < (layout == QG_TN ? M : K) || ldb < (layout == QG_NT ? K : N)) return QG_ERR_SHAPE;
+    if (!aligned(A, esize) || !aligned(B, esize)) return QG_ERR_ALIGN;
+  }
+  qg::GroupedArgs a{layout, dtype, groups, layout == QG_TN ? K : M, offsets, M, N, K, (const uint16_t*)A, lda,
+                    (const uint16_t*)B, ldb, stride_b, (uint16_t*)C, ldc, stride_c};
+  if (qg::grouped_threads(a) >= (int64_t)1 << 32) return QG_ERR_SHAPE;
+  return hip_status(qg::launch_grouped(a, (hipStream_t)stream));
 }
 
 int32_t qg_probe_copy(const void* src, void* dst, int64_t bytes, int64_t blocks, void* stream) {

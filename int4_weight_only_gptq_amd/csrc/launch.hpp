@@ -102,6 +102,24 @@ struct BatchStrides {
 
 hipError_t launch_dense(const DenseArgs& a, hipStream_t stream);
 
+// Dense products grouped by expert.  NT / NN: M rows sorted by group, B + e sb for
+// group e; TN: K rows sorted by group, C + e sc for group e.  offsets [groups + 1].
+struct GroupedArgs {
+  int layout, dtype;
+  int64_t groups, rows;    // rows: M (NT, NN) or K (TN)
+  const int32_t* offsets;
+  int64_t M, N, K;
+  const uint16_t* A;
+  int64_t lda;
+  const uint16_t* B;
+  int64_t ldb, sb;
+  uint16_t* C;
+  int64_t ldc, sc;
+};
+// Threads of the launch that launch_grouped would make (grids hold fewer than 2^32).
+int64_t grouped_threads(const GroupedArgs& a);
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+
 // register-resident bf16 MFMA loop with clock stamps (measurement probe)
 hipError_t launch_mfma_probe(int64_t blocks, int iters, uint64_t* clocks, hipStream_t stream);
 // 16-byte copy and read-only streams over `bytes` (measurement probes); blocks 0 = automatic
