@@ -58,6 +58,33 @@ int32_t gemm_grouped(int32_t layout, int32_t dtype, int64_t groups, const int32_
                      int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b, void* C,
                      int64_t ldc, int64_t stride_c, void* stream);
 
+/*
+ * qgemm_int4_grouped -- qgemm_int4 with a weight per expert:
+ *
+ *   Y[r] = X[r] . dequant(W_e)^T for the rows r of expert e,
+ *
+ * the storage of qgemm_int4 once per expert, back to back: qweight
+ * [experts][k/8][n], scales [experts][k/128][n], qzeros [experts][k/128][n/8] or
+ * NULL; x bf16 [m][ldx], y bf16 [m][ldy].  offsets [experts + 1] as above (the
+ * grouped rows are the m rows).  Limits, alignments, rounding and errors of x, y
+ * and the weights as qgemm_int4; k == 0 writes zeros to the experts' rows.
+ *
+ *   workspace, workspace_bytes
+ *            optional device scratch (16-byte aligned) of
+ *            qgemm_int4_grouped_workspace_size bytes, which holds the activations in
+ *            the decode's order and their sums during the call (its contents need no
+ *            initialisation and are not kept).  With NULL or fewer bytes the
+ *            product does both itself, slower.  Calls that share a workspace must
+ *            not overlap.
+ */
+int32_t qgemm_int4_grouped(const void* x, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
+                           const uint32_t* qzeros, int64_t experts, const int32_t* offsets, void* y, int64_t ldy,
+                           int64_t m, int64_t n, int64_t k, int32_t group_size, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes qgemm_int4_grouped can use (0: none); < 0: -error. */
+int64_t qgemm_int4_grouped_workspace_size(int64_t experts, int64_t m, int64_t n, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

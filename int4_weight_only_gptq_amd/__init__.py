@@ -13,7 +13,7 @@ import os
 
 __all__ = ["load", "lib_path", "QGemmError", "qgemm_int4", "qgemm_int4_noalloc", "qgemm_int4_lora",
            "qgemm_int4_epilogue", "qgemm_int4_dequant", "gemm_dense",
-           "gemm_dense_batched", "gemm_grouped", "describe_int4",
+           "gemm_dense_batched", "gemm_grouped", "qgemm_int4_grouped", "describe_int4",
            "workspace_size", "probe_mfma_bf16", "probe_copy", "probe_read",
            "abi_version", "PATHS", "LAYOUTS"]
 
@@ -91,6 +91,10 @@ def load():
     lib.gemm_dense_batched.restype = i32
     lib.gemm_dense_batched.argtypes = [i32, i32, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64,
                                        i64, vp]
+    lib.qgemm_int4_grouped.restype = i32
+    lib.qgemm_int4_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, vp, i64, vp]
+    lib.qgemm_int4_grouped_workspace_size.restype = i64
+    lib.qgemm_int4_grouped_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.gemm_grouped.restype = i32
     lib.gemm_grouped.argtypes = [i32, i32, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp]
     lib.qg_probe_mfma_bf16.restype = i32
@@ -435,9 +439,9 @@ def _same_device(first, *others):
 
 def _rows_ld(t, what):
     """Distance in elements between the rows of a matrix, or of each matrix of a stack."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
         raise ValueError("the last dimension of %s must be contiguous" % what)
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+    return t.stride(-2) if t.shape[-2] > 1 and t.numel() else max(t.stride(-2), t.shape[-1])
 
 
 def _group_count(offsets):
@@ -489,6 +493,49 @@ def gemm_grouped(layout: str, a, b, offsets, out=None, stream=None):
                               _rows_ld(a, "a"), b.data_ptr(), _rows_ld(b, "b"), sb, out.data_ptr(),
                               _rows_ld(out, "out"), sc, _stream(a, stream))
     _check(st, "gemm_grouped")
+    return out
+
+
+def qgemm_int4_grouped(x, qweight, scales, qzeros, offsets, out=None, group_size: int = 128, workspace=None,
+                       stream=None):
+    """qgemm_int4 with a weight per expert: out[r] (bf16) = x[r] . dequant(W_e)^T for the rows
+    offsets[e] .. offsets[e + 1] - 1 of expert e (see gemm_grouped and qgemm_grouped.h).
+
+    qweight int32/uint32 [experts][k/8][n]; scales fp16 [experts][k/128][n]; qzeros int32/uint32
+    [experts][k/128][n/8], or None; all contiguous.  ``workspace``: None = scratch allocated for
+    the call where the product uses some; False = none (slower); or a caller-owned uint8 tensor."""
+    import torch
+
+    lib = load()
+    m, k = x.shape
+    experts = _group_count(offsets)
+    n = qweight.shape[-1]
+    if x.dtype != torch.bfloat16 or scales.dtype != torch.float16 or qweight.element_size() != 4:
+        raise TypeError("x must be bfloat16, scales float16 and qweight 32-bit words")
+    if tuple(qweight.shape) != (experts, k // 8, n) or tuple(scales.shape) != (experts, k // 128, n):
+        raise ValueError("qweight must be [experts][k/8][n] and scales [experts][k/128][n]")
+    if qzeros is not None and (tuple(qzeros.shape) != (experts, k // 128, n // 8) or qzeros.element_size() != 4):
+        raise ValueError("qzeros must be 32-bit words [experts][k/128][n/8]")
+    for t in (qweight, scales, qzeros):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("qweight, scales and qzeros must be contiguous")
+    _same_device(x, qweight, scales, qzeros, offsets, out)
+    with _launch_on(x.device, stream):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+        elif tuple(out.shape) != (m, n) or out.dtype != torch.bfloat16:
+            raise ValueError("out must be bfloat16 [m][n]")
+        if workspace is None:
+            size = lib.qgemm_int4_grouped_workspace_size(experts, m, n, k)
+            if size < 0:
+                raise QGemmError(-size, "qgemm_int4_grouped_workspace_size")
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else False
+        wptr = None if workspace is False else workspace.data_ptr()
+        wbytes = 0 if workspace is False else workspace.numel() * workspace.element_size()
+        st = lib.qgemm_int4_grouped(x.data_ptr(), _rows_ld(x, "x"), qweight.data_ptr(), scales.data_ptr(),
+                                    _ptr(qzeros), experts, offsets.data_ptr(), out.data_ptr(),
+                                    _rows_ld(out, "out"), m, n, k, group_size, wptr, wbytes, _stream(x, stream))
+    _check(st, "qgemm_int4_grouped")
     return out
 
 

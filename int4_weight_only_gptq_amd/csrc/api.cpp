@@ -441,6 +441,49 @@ int32_t gemm_grouped(int32_t layout, int32_t dtype, int64_t groups, const int32_
   return hip_status(qg::launch_grouped(a, (hipStream_t)stream));
 }
 
+// Sizes of a grouped int4 product; QG_OK or the error.
+static int32_t check_int4_grouped(int64_t experts, int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 0 || experts < 0 || k % 128 != 0 || n % 8 != 0) return QG_ERR_SHAPE;
+  if (n > (int64_t)1 << 26 || k > (int64_t)1 << 22 || m > kMaxGroupedSize || experts > QG_MAX_GROUPS)
+    return QG_ERR_SHAPE;
+  if (m == 0 || n == 0 || k == 0 || experts == 0) return QG_OK;
+  // grids hold fewer than 2^32 threads (the preparation runs m k / 8 of them)
+  if (qg::int4_grouped_threads(experts, m, n, k) >= (int64_t)1 << 32 || m * (k / 8) >= (int64_t)1 << 32)
+    return QG_ERR_SHAPE;
+  return QG_OK;
+}
+
+int64_t qgemm_int4_grouped_workspace_size(int64_t experts, int64_t m, int64_t n, int64_t k) {
+  const int32_t st = check_int4_grouped(experts, m, n, k);
+  if (st != QG_OK) return -(int64_t)st;
+  if (m == 0 || n == 0 || k == 0 || experts == 0) return 0;
+  return qg::int4_grouped_workspace(experts, m, n, k);
+}
+
+int32_t qgemm_int4_grouped(const void* x, int64_t ldx, const uint32_t* qweight, const uint16_t* scales,
+                           const uint32_t* qzeros, int64_t experts, const int32_t* offsets, void* y, int64_t ldy,
+                           int64_t m, int64_t n, int64_t k, int32_t group_size, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  int32_t st = check_int4_grouped(experts, m, n, k);
+  if (st != QG_OK) return st;
+  st = check_int4(x, ldx, qweight, scales, qzeros, y, ldy, m, n, k, group_size);
+  if (st != QG_OK) return st;
+  if (workspace_bytes < 0) return QG_ERR_SHAPE;
+  if (workspace != nullptr && !aligned(workspace, 16)) return QG_ERR_ALIGN;
+  if (m == 0 || n == 0 || experts == 0) return QG_OK;
+  if (offsets == nullptr) return QG_ERR_NULL;
+  if (!aligned(offsets, 4)) return QG_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  if (k == 0) {   // zeros in the experts' rows: the dense product of k = 0
+    const qg::GroupedArgs g{QG_NT, QG_BF16, experts, m, offsets, m, n, 0, nullptr, 0, nullptr, 0, 0,
+                            (uint16_t*)y, ldy, 0};
+    return hip_status(qg::launch_grouped(g, s));
+  }
+  const qg::Int4GroupedArgs a{(const uint16_t*)x, ldx, qweight, scales, qzeros, experts, offsets, (uint16_t*)y, ldy,
+                              m, n, k};
+  return hip_status(qg::launch_int4_grouped(a, workspace, workspace_bytes, s));
+}
+
 int32_t qg_probe_copy(const void* src, void* dst, int64_t bytes, int64_t blocks, void* stream) {
   if (bytes < 0 || bytes % 16 != 0 || blocks < 0 || blocks > 65536) return QG_ERR_SHAPE;
   if (bytes == 0) return QG_OK;

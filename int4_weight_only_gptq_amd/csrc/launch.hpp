@@ -120,6 +120,24 @@ struct GroupedArgs {
 int64_t grouped_threads(const GroupedArgs& a);
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
 
+// int4 products grouped by expert: m rows sorted by expert, the weights of all
+// experts back to back.  offsets [experts + 1].
+struct Int4GroupedArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint32_t* qweight;
+  const uint16_t* scales;
+  const uint32_t* qzeros;
+  int64_t experts;
+  const int32_t* offsets;
+  uint16_t* y;
+  int64_t ldy;
+  int64_t m, n, k;
+};
+int64_t int4_grouped_threads(int64_t experts, int64_t m, int64_t n, int64_t k);
+int64_t int4_grouped_workspace(int64_t experts, int64_t m, int64_t n, int64_t k);
+hipError_t launch_int4_grouped(const Int4GroupedArgs& a, void* ws, int64_t ws_bytes, hipStream_t stream);
+
 // register-resident bf16 MFMA loop with clock stamps (measurement probe)
 hipError_t launch_mfma_probe(int64_t blocks, int iters, uint64_t* clocks, hipStream_t stream);
 // 16-byte copy and read-only streams over `bytes` (measurement probes); blocks 0 = automatic

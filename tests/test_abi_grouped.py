@@ -52,3 +52,30 @@ def grouped(lib, layout=0, dtype=0, groups=4, off=A16, M=32, N=16, K=64, A=A16, 
 ])
 def test_grouped_rejects_invalid_arguments(lib, kw, code):
     assert grouped(lib, **kw) == code
+
+
+def int4(lib, x=A16, ldx=256, qw=A16, sc=A16, qz=A16, experts=4, off=A16, y=A16, ldy=64, m=8, n=64, k=256, gs=128,
+         ws=None, wsb=0):
+    return lib.qgemm_int4_grouped(x, ldx, qw, sc, qz, experts, off, y, ldy, m, n, k, gs, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(m=-1), SHAPE), (dict(n=-8), SHAPE), (dict(k=-128), SHAPE), (dict(experts=-1), SHAPE),
+    (dict(experts=4097), SHAPE), (dict(k=200), SHAPE), (dict(n=60), SHAPE), (dict(gs=64), UNSUP),
+    (dict(x=0), NULL), (dict(qw=0), NULL), (dict(sc=0), NULL), (dict(y=0), NULL), (dict(off=0), NULL),
+    (dict(ldx=128), SHAPE), (dict(ldy=32), SHAPE), (dict(x=A16 + 2), ALIGN), (dict(qw=A16 + 4), ALIGN),
+    (dict(sc=A16 + 2), ALIGN), (dict(qz=A16 + 2), ALIGN), (dict(y=A16 + 2), ALIGN), (dict(off=A16 + 2), ALIGN),
+    (dict(ws=A16 + 8, wsb=64), ALIGN), (dict(wsb=-1), SHAPE),
+    (dict(m=1 << 30, n=1 << 26, ldy=1 << 26, k=1 << 20, ldx=1 << 20), SHAPE),      # more than a grid holds
+    (dict(m=0, x=0, qw=0, sc=0, qz=0, y=0, off=0), OK), (dict(experts=0), OK), (dict(n=0, ldy=0), OK),
+])
+def test_int4_grouped_rejects_invalid_arguments(lib, kw, code):
+    assert int4(lib, **kw) == code
+
+
+def test_int4_grouped_workspace_size(lib):
+    f = lib.qgemm_int4_grouped_workspace_size
+    assert f(64, 64, 1024, 2048) == 0                                         # strips use none
+    assert f(8, 4096, 14336, 4096) == 4096 * 4096 * 2 + 32 * 4096 * 4         # activations and their sums
+    assert f(0, 8, 64, 256) == 0 and f(4, 0, 64, 256) == 0
+    assert f(4, 8, 60, 256) == -SHAPE and f(4, 8, 64, 100) == -SHAPE and f(-1, 8, 64, 256) == -SHAPE
