@@ -13,7 +13,8 @@ import os
 
 __all__ = ["load", "lib_path", "QGemmError", "qgemm_int4", "qgemm_int4_noalloc", "qgemm_int4_lora",
            "qgemm_int4_epilogue", "qgemm_int4_dequant", "gemm_dense",
-           "gemm_dense_batched", "gemm_grouped", "qgemm_int4_grouped", "describe_int4",
+           "gemm_dense_batched", "gemm_grouped", "qgemm_int4_grouped", "mxfp4_quantize",
+           "mxfp4_dequantize", "gemm_mxfp4", "describe_int4",
            "workspace_size", "probe_mfma_bf16", "probe_copy", "probe_read",
            "abi_version", "PATHS", "LAYOUTS"]
 
@@ -95,6 +96,12 @@ def load():
     lib.qgemm_int4_grouped.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, vp, i64, vp]
     lib.qgemm_int4_grouped_workspace_size.restype = i64
     lib.qgemm_int4_grouped_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.mxfp4_quantize.restype = i32
+    lib.mxfp4_quantize.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.mxfp4_dequantize.restype = i32
+    lib.mxfp4_dequantize.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_mxfp4.restype = i32
+    lib.gemm_mxfp4.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
     lib.gemm_grouped.restype = i32
     lib.gemm_grouped.argtypes = [i32, i32, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp]
     lib.qg_probe_mfma_bf16.restype = i32
@@ -536,6 +543,104 @@ def qgemm_int4_grouped(x, qweight, scales, qzeros, offsets, out=None, group_size
                                     _ptr(qzeros), experts, offsets.data_ptr(), out.data_ptr(),
                                     _rows_ld(out, "out"), m, n, k, group_size, wptr, wbytes, _stream(x, stream))
     _check(st, "qgemm_int4_grouped")
+    return out
+
+
+def _dtype_name(dtype):
+    import torch
+
+    names = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
+    if dtype not in names:
+        raise TypeError("the dtype must be bfloat16, float16 or float32")
+    return names[dtype]
+
+
+def _mx_matrix(codes, scales, what):
+    """(rows, k) of an MXFP4 matrix; raises unless codes and scales fit together."""
+    import torch
+
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("%s: codes and scales must be uint8" % what)
+    if codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError("%s: codes must be [rows][k/2] and scales [rows][k/32]" % what)
+    rows, k = codes.shape[0], 2 * codes.shape[1]
+    if k % 32 or tuple(scales.shape) != (rows, k // 32):
+        raise ValueError("%s: codes must be [rows][k/2] and scales [rows][k/32], k a multiple of 32" % what)
+    return rows, k
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """(codes uint8 [rows][k/2], scales uint8 [rows][k/32]) of x [rows][k] (bf16, fp16 or fp32,
+    k a multiple of 32) in MXFP4: blocks of 32 along a row with one power-of-two scale, 4-bit
+    e2m1 codes (see qgemm_mxfp4.h for the rounding).  New scales have rows that start on 16
+    bytes (a view of padded rows when k is not a multiple of 512)."""
+    import torch
+
+    lib = load()
+    name = _dtype_name(x.dtype)
+    if x.dim() != 2 or x.shape[1] % 32:
+        raise ValueError("x must be [rows][k] with k a multiple of 32")
+    rows, k = x.shape
+    _same_device(x, codes, scales)
+    with _launch_on(x.device, stream):
+        if codes is None:
+            codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty((rows, (k // 32 + 15) // 16 * 16), dtype=torch.uint8, device=x.device)[:, :k // 32]
+        if _mx_matrix(codes, scales, "mxfp4_quantize") != (rows, k):
+            raise ValueError("codes must be [rows][k/2] and scales [rows][k/32]")
+        st = lib.mxfp4_quantize(_DTYPES[name], rows, k, x.data_ptr(), _rows_ld(x, "x"), codes.data_ptr(),
+                                _rows_ld(codes, "codes"), scales.data_ptr(), _rows_ld(scales, "scales"),
+                                _stream(x, stream))
+    _check(st, "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
+    """The values [rows][k] of an MXFP4 matrix in dtype (bfloat16 when neither it nor out is given)."""
+    import torch
+
+    lib = load()
+    rows, k = _mx_matrix(codes, scales, "mxfp4_dequantize")
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    name = _dtype_name(dtype)
+    _same_device(codes, scales, out)
+    with _launch_on(codes.device, stream):
+        if out is None:
+            out = torch.empty((rows, k), dtype=dtype, device=codes.device)
+        elif tuple(out.shape) != (rows, k) or out.dtype != dtype:
+            raise ValueError("out must be [rows][k] of dtype")
+        st = lib.mxfp4_dequantize(_DTYPES[name], rows, k, codes.data_ptr(), _rows_ld(codes, "codes"),
+                                  scales.data_ptr(), _rows_ld(scales, "scales"), out.data_ptr(),
+                                  _rows_ld(out, "out"), _stream(codes, stream))
+    _check(st, "mxfp4_dequantize")
+    return out
+
+
+def gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, stream=None):
+    """out [M][N] = A . B^T of two MXFP4 matrices A [M][K] and B [N][K] (mxfp4_quantize's codes and
+    scales), summed in fp32 and rounded once to dtype (bfloat16 when neither it nor out is given)."""
+    import torch
+
+    lib = load()
+    (M, K), (N, kb) = _mx_matrix(a_codes, a_scales, "a"), _mx_matrix(b_codes, b_scales, "b")
+    if K != kb:
+        raise ValueError("A and B must have the same k")
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    name = _dtype_name(dtype)
+    _same_device(a_codes, a_scales, b_codes, b_scales, out)
+    with _launch_on(a_codes.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
+        elif tuple(out.shape) != (M, N) or out.dtype != dtype:
+            raise ValueError("out must be [M][N] of dtype")
+        st = lib.gemm_mxfp4(_DTYPES[name], M, N, K, a_codes.data_ptr(), _rows_ld(a_codes, "a_codes"),
+                            a_scales.data_ptr(), _rows_ld(a_scales, "a_scales"), b_codes.data_ptr(),
+                            _rows_ld(b_codes, "b_codes"), b_scales.data_ptr(), _rows_ld(b_scales, "b_scales"),
+                            out.data_ptr(), _rows_ld(out, "out"), _stream(a_codes, stream))
+    _check(st, "gemm_mxfp4")
     return out
 
 

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libqgemm_gfx950.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "int4_kernels.hip", "dense_kernels.hip", "grouped_kernels.hip", "grouped_int4_kernels.hip",
-           "probes.hip"]
+           "mxfp4_kernels.hip", "probes.hip"]
 # per-source flags: the MFMA probe keeps its accumulator chains in VGPRs (with
 # AGPR accumulators this compiler shuffled them between iterations); the
 # product kernels keep the default form, whose k loops carry no such moves

@@ -2,6 +2,7 @@
 // Declarations and the contract of each entry point are in include/qgemm.h.
 #include "qgemm.h"
 #include "qgemm_grouped.h"
+#include "qgemm_mxfp4.h"
 
 #include <hip/hip_runtime.h>
 #include <stdio.h>
@@ -30,7 +31,7 @@ int32_t hip_status(hipError_t e) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Sizes of the grouped products: rows and tiles are counted in 32 bits.
+// Sizes of the grouped and MXFP4 products: rows and tiles are counted in 32 bits.
 constexpr int64_t kMaxGroupedSize = ((int64_t)1 << 31) - 1024;
 
 // Validation shared by the int4 entry points; returns QG_OK or the error.
@@ -439,6 +440,62 @@ int32_t gemm_grouped(int32_t layout, int32_t dtype, int64_t groups, const int32_
                     (const uint16_t*)B, ldb, stride_b, (uint16_t*)C, ldc, stride_c};
   if (qg::grouped_threads(a) >= (int64_t)1 << 32) return QG_ERR_SHAPE;
   return hip_status(qg::launch_grouped(a, (hipStream_t)stream));
+}
+
+// An MXFP4 matrix of rows of k elements; QG_OK or the error.
+static int32_t check_mxfp4(int64_t k, const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                           int64_t ld_scales) {
+  if (codes == nullptr || scales == nullptr) return QG_ERR_NULL;
+  if (ld_codes < k / 2 || ld_scales < k / 32) return QG_ERR_SHAPE;
+  if (!aligned(codes, 16) || ld_codes % 16 != 0) return QG_ERR_ALIGN;
+  return QG_OK;
+}
+
+static int32_t check_mxfp4_convert(int32_t dtype, int64_t rows, int64_t k, const void* x, int64_t ldx,
+                                   const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales) {
+  if (dtype != QG_BF16 && dtype != QG_FP16 && dtype != QG_FP32) return QG_ERR_DTYPE;
+  if (rows < 0 || k < 0 || k % 32 != 0) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;
+  if (rows > (((int64_t)1 << 35) - 1) / k || ldx < k) return QG_ERR_SHAPE;   // eight elements a thread, < 2^32 threads
+  if (x == nullptr) return QG_ERR_NULL;
+  if (!aligned(x, dtype == QG_FP32 ? 4 : 2)) return QG_ERR_ALIGN;
+  return check_mxfp4(k, codes, ld_codes, scales, ld_scales);
+}
+
+int32_t mxfp4_quantize(int32_t dtype, int64_t rows, int64_t k, const void* x, int64_t ldx, uint8_t* codes,
+                       int64_t ld_codes, uint8_t* scales, int64_t ld_scales, void* stream) {
+  const int32_t st = check_mxfp4_convert(dtype, rows, k, x, ldx, codes, ld_codes, scales, ld_scales);
+  if (st != QG_OK || rows == 0 || k == 0) return st;
+  return hip_status(qg::launch_mxfp4_quantize(dtype, x, ldx, rows, k, codes, ld_codes, scales, ld_scales,
+                                              (hipStream_t)stream));
+}
+
+int32_t mxfp4_dequantize(int32_t dtype, int64_t rows, int64_t k, const uint8_t* codes, int64_t ld_codes,
+                         const uint8_t* scales, int64_t ld_scales, void* y, int64_t ldy, void* stream) {
+  const int32_t st = check_mxfp4_convert(dtype, rows, k, y, ldy, codes, ld_codes, scales, ld_scales);
+  if (st != QG_OK || rows == 0 || k == 0) return st;
+  return hip_status(qg::launch_mxfp4_dequantize(dtype, codes, ld_codes, scales, ld_scales, rows, k, y, ldy,
+                                                (hipStream_t)stream));
+}
+
+int32_t gemm_mxfp4(int32_t dtype, int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda,
+                   const uint8_t* a_scales, int64_t lda_scales, const uint8_t* b, int64_t ldb,
+                   const uint8_t* b_scales, int64_t ldb_scales, void* c, int64_t ldc, void* stream) {
+  if (dtype != QG_BF16 && dtype != QG_FP16 && dtype != QG_FP32) return QG_ERR_DTYPE;
+  if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return QG_ERR_SHAPE;
+  if (M > kMaxGroupedSize || N > kMaxGroupedSize || K > kMaxGroupedSize) return QG_ERR_SHAPE;
+  if (M == 0 || N == 0) return QG_OK;
+  if (c == nullptr) return QG_ERR_NULL;
+  if (ldc < N) return QG_ERR_SHAPE;
+  if (!aligned(c, dtype == QG_FP32 ? 4 : 2)) return QG_ERR_ALIGN;
+  if (K > 0) {
+    int32_t st = check_mxfp4(K, a, lda, a_scales, lda_scales);
+    if (st == QG_OK) st = check_mxfp4(K, b, ldb, b_scales, ldb_scales);
+    if (st != QG_OK) return st;
+  }
+  const qg::MxGemmArgs g{M, N, K, a, lda, a_scales, lda_scales, b, ldb, b_scales, ldb_scales, c, ldc};
+  if (qg::mxfp4_threads(g) >= (int64_t)1 << 32) return QG_ERR_SHAPE;
+  return hip_status(qg::launch_mxfp4_gemm(dtype, g, (hipStream_t)stream));
 }
 
 // Sizes of a grouped int4 product; QG_OK or the error.

@@ -195,6 +195,9 @@ __device__ __forceinline__ void wait_vmcnt(int n) {
   }
 }
 
+// 16 zero bytes: what a direct load takes for a chunk past the end of k.
+__device__ const u32x4 kZeroChunk = {0u, 0u, 0u, 0u};
+
 // Slot of 16-byte chunk c (8 bf16 of k) of row r in a K-contiguous LDS tile of
 // 8 chunks per row: the XOR spreads the 16 rows one MFMA operand read touches
 // over distinct banks.

@@ -9,9 +9,6 @@ namespace qg {
 
 constexpr int DBK = 64;
 
-// 16 zero bytes: what a lane loads for a chunk past the end of k
-__device__ const u32x4 kZeroChunk = {0u, 0u, 0u, 0u};
-
 // Pipeline kernel for all three layouts (K % 64 == 0, operands 16-byte
 // vectorizable).  Tile BM x BN per workgroup of 4 waves (2 x 2, each
 // (BM/2) x (BN/2)), k tiles of 64 in a STAGES-deep ring of LDS buffers filled

@@ -138,6 +138,28 @@ int64_t int4_grouped_threads(int64_t experts, int64_t m, int64_t n, int64_t k);
 int64_t int4_grouped_workspace(int64_t experts, int64_t m, int64_t n, int64_t k);
 hipError_t launch_int4_grouped(const Int4GroupedArgs& a, void* ws, int64_t ws_bytes, hipStream_t stream);
 
+// MXFP4: quantisation, reading back, and C = A . B^T (leading dimensions of codes and
+// scales in bytes, of c in elements).
+hipError_t launch_mxfp4_quantize(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t k, uint8_t* codes,
+                                 int64_t ldc, uint8_t* scales, int64_t lds, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(int dtype, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                                   int64_t rows, int64_t k, void* y, int64_t ldy, hipStream_t stream);
+struct MxGemmArgs {
+  int64_t M, N, K;
+  const uint8_t* a;
+  int64_t lda;
+  const uint8_t* as;
+  int64_t ldas;
+  const uint8_t* b;
+  int64_t ldb;
+  const uint8_t* bs;
+  int64_t ldbs;
+  void* c;
+  int64_t ldc;
+};
+int64_t mxfp4_threads(const MxGemmArgs& g);
+hipError_t launch_mxfp4_gemm(int dtype, const MxGemmArgs& g, hipStream_t stream);
+
 // register-resident bf16 MFMA loop with clock stamps (measurement probe)
 hipError_t launch_mfma_probe(int64_t blocks, int iters, uint64_t* clocks, hipStream_t stream);
 // 16-byte copy and read-only streams over `bytes` (measurement probes); blocks 0 = automatic
