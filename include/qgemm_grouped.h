@@ -48,7 +48,7 @@ extern "C" {
  * element's size are accepted (sizes below 2^31 - 1024, groups <= QG_MAX_GROUPS,
  * and at most 2^32 threads over all tiles); bf16 / fp16 take 16-byte loads when
  * A and B are 16-byte aligned and their contiguous extents, leading dimensions
- * and stride_b are multiples of 8 elements.  M, N or groups of zero enqueue
+ * and stride_b are multiples of 8 elements (leading dimensions up to 2^21, C's too).  M, N or groups of zero enqueue
  * nothing; K of zero (NT, NN) writes zeros to the groups' rows.  C must not
  * overlap A, B or offsets.
  * Errors: QG_ERR_NULL, QG_ERR_SHAPE, QG_ERR_ALIGN, QG_ERR_DTYPE, QG_ERR_LAYOUT,

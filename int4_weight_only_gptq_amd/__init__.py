@@ -42,10 +42,14 @@ def lib_path() -> str:
 
 def load():
     """Load the built library (binds to the HIP runtime torch has loaded)."""
-    global _lib
+    global _lib, _raw_stream
     if _lib is not None:
         return _lib
-    import torch  # noqa: F401  -- the library must share torch's HIP runtime
+    import torch  # the library must share torch's HIP runtime
+
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _type_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
 
     path = lib_path()
     if not os.path.exists(path):
@@ -425,30 +429,46 @@ def gemm_dense_batched(layout: str, a, b, out=None, stream=None):
     return out
 
 
-def _launch_on(device, stream):
-    """Context of a call: its tensors' device is current, and new tensors are allocated on
-    the launch stream (so that the caching allocator orders their reuse with the call)."""
-    import contextlib
+# The grouped and MXFP4 calls are short enough on the device for the host's part to count,
+# so their wrappers keep to the cheapest forms: sizes, strides and device numbers as plain
+# integers, and torch's raw stream handle (_raw_stream and _type_codes are set by load()).
+_raw_stream = None
+_type_codes = {}
+
+
+def _elsewhere(device_index, stream):
+    """Whether a call needs _launch_on: a stream of the caller's, or another device than the current one."""
     import torch
 
-    if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    return torch.cuda.stream(_torch_stream(device, stream))
+    return stream is not None or torch.cuda.current_device() != device_index
 
 
-def _same_device(first, *others):
-    if first.device.type != "cuda":
+def _launch_on(tensor, stream):
+    """Context of a call: its tensors' device is current, and new tensors are allocated on
+    the launch stream (so that the caching allocator orders their reuse with the call)."""
+    import torch
+
+    return (torch.cuda.device(tensor.device) if stream is None
+            else torch.cuda.stream(_torch_stream(tensor.device, stream)))
+
+
+def _device_of(first, *others):
+    """Device number of tensors that must share a GPU (None is left out)."""
+    d = first.get_device()
+    if d < 0:
         raise ValueError("expected tensors on a GPU")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError("all tensors must be on one device")
+    return d
 
 
 def _rows_ld(t, what):
     """Distance in elements between the rows of a matrix, or of each matrix of a stack."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+    st, sh = t.stride(), t.shape
+    if st[-1] != 1 and sh[-1] > 1 and t.numel():
         raise ValueError("the last dimension of %s must be contiguous" % what)
-    return t.stride(-2) if t.shape[-2] > 1 and t.numel() else max(t.stride(-2), t.shape[-1])
+    return st[-2] if st[-2] >= sh[-1] or (sh[-2] > 1 and t.numel()) else sh[-1]
 
 
 def _group_count(offsets):
@@ -470,36 +490,42 @@ def gemm_grouped(layout: str, a, b, offsets, out=None, stream=None):
 
     Rows outside every group are left as they were in ``out`` (a new ``out`` is not
     initialised there).  Nothing is read back to the host."""
-    import torch
+    device = _device_of(a, b, offsets, out)
+    if _elsewhere(device, stream):
+        with _launch_on(a, stream):
+            return _gemm_grouped(layout, a, b, offsets, out, device)
+    return _gemm_grouped(layout, a, b, offsets, out, device)
 
-    lib = load()
+
+def _gemm_grouped(layout, a, b, offsets, out, device):
+    lib = _lib or load()
     dtype = _dtype_of(a, b)
     groups = _group_count(offsets)
+    if a.dim() != 2:
+        raise ValueError("a must be a matrix")
     if layout == "TN":
-        if a.dim() != 2 or b.dim() != 2 or a.shape[0] != b.shape[0]:
+        if b.dim() != 2 or a.shape[0] != b.shape[0]:
             raise ValueError("TN: a must be [rows][M] and b [rows][N]")
-        (K, M), N = a.shape, b.shape[1]
-        shape, sb = (groups, M, N), 0
-    elif layout in ("NT", "NN"):
-        M, K = a.shape if a.dim() == 2 else (-1, -1)
+        (K, M), N, sb = a.shape, b.shape[1], 0
+        shape = (groups, M, N)
+    elif layout == "NT" or layout == "NN":
+        M, K = a.shape
         if b.dim() != 3 or b.shape[0] != groups or b.shape[2 if layout == "NT" else 1] != K:
             raise ValueError("%s: a must be [rows][K] and b [groups]%s" %
                              (layout, "[N][K]" if layout == "NT" else "[K][N]"))
-        N = b.shape[1 if layout == "NT" else 2]
-        shape, sb = (M, N), b.stride(0)
+        N, sb = b.shape[1 if layout == "NT" else 2], b.stride(0)
+        shape = (M, N)
     else:
         raise ValueError(layout)
-    _same_device(a, b, offsets, out)
-    with _launch_on(a.device, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=a.dtype, device=a.device)
-        elif tuple(out.shape) != shape or out.dtype != a.dtype:
-            raise ValueError("out must be %s of the operands' dtype" % (list(shape),))
-        sc = out.stride(0) if layout == "TN" else 0
-        st = lib.gemm_grouped(LAYOUTS[layout], _DTYPES[dtype], groups, offsets.data_ptr(), M, N, K, a.data_ptr(),
-                              _rows_ld(a, "a"), b.data_ptr(), _rows_ld(b, "b"), sb, out.data_ptr(),
-                              _rows_ld(out, "out"), sc, _stream(a, stream))
-    _check(st, "gemm_grouped")
+    if out is None:
+        out = a.new_empty(shape)
+    elif tuple(out.shape) != shape or out.dtype != a.dtype:
+        raise ValueError("out must be %s of the operands' dtype" % (list(shape),))
+    st = lib.gemm_grouped(LAYOUTS[layout], _DTYPES[dtype], groups, offsets.data_ptr(), M, N, K, a.data_ptr(),
+                          _rows_ld(a, "a"), b.data_ptr(), _rows_ld(b, "b"), sb, out.data_ptr(),
+                          _rows_ld(out, "out"), out.stride(0) if layout == "TN" else 0, _raw_stream(device))
+    if st:
+        raise QGemmError(st, "gemm_grouped")
     return out
 
 
@@ -511,48 +537,57 @@ def qgemm_int4_grouped(x, qweight, scales, qzeros, offsets, out=None, group_size
     qweight int32/uint32 [experts][k/8][n]; scales fp16 [experts][k/128][n]; qzeros int32/uint32
     [experts][k/128][n/8], or None; all contiguous.  ``workspace``: None = scratch allocated for
     the call where the product uses some; False = none (slower); or a caller-owned uint8 tensor."""
+    device = _device_of(x, qweight, scales, qzeros, offsets, out, None if workspace is False else workspace)
+    if _elsewhere(device, stream):
+        with _launch_on(x, stream):
+            return _int4_grouped(x, qweight, scales, qzeros, offsets, out, group_size, workspace, device)
+    return _int4_grouped(x, qweight, scales, qzeros, offsets, out, group_size, workspace, device)
+
+
+def _int4_grouped(x, qweight, scales, qzeros, offsets, out, group_size, workspace, device):
     import torch
 
-    lib = load()
-    m, k = x.shape
+    lib = _lib or load()
     experts = _group_count(offsets)
-    n = qweight.shape[-1]
+    if x.dim() != 2 or qweight.dim() != 3:
+        raise ValueError("x must be [m][k] and qweight [experts][k/8][n]")
+    (m, k), n = x.shape, qweight.shape[2]
     if x.dtype != torch.bfloat16 or scales.dtype != torch.float16 or qweight.element_size() != 4:
         raise TypeError("x must be bfloat16, scales float16 and qweight 32-bit words")
-    if tuple(qweight.shape) != (experts, k // 8, n) or tuple(scales.shape) != (experts, k // 128, n):
+    if qweight.shape != (experts, k // 8, n) or scales.shape != (experts, k // 128, n):
         raise ValueError("qweight must be [experts][k/8][n] and scales [experts][k/128][n]")
-    if qzeros is not None and (tuple(qzeros.shape) != (experts, k // 128, n // 8) or qzeros.element_size() != 4):
-        raise ValueError("qzeros must be 32-bit words [experts][k/128][n/8]")
-    for t in (qweight, scales, qzeros):
-        if t is not None and not t.is_contiguous():
+    if not (qweight.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("qweight, scales and qzeros must be contiguous")
+    if qzeros is not None:
+        if qzeros.shape != (experts, k // 128, n // 8) or qzeros.element_size() != 4:
+            raise ValueError("qzeros must be 32-bit words [experts][k/128][n/8]")
+        if not qzeros.is_contiguous():
             raise ValueError("qweight, scales and qzeros must be contiguous")
-    _same_device(x, qweight, scales, qzeros, offsets, out)
-    with _launch_on(x.device, stream):
-        if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
-        elif tuple(out.shape) != (m, n) or out.dtype != torch.bfloat16:
-            raise ValueError("out must be bfloat16 [m][n]")
-        if workspace is None:
-            size = lib.qgemm_int4_grouped_workspace_size(experts, m, n, k)
-            if size < 0:
-                raise QGemmError(-size, "qgemm_int4_grouped_workspace_size")
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else False
-        wptr = None if workspace is False else workspace.data_ptr()
-        wbytes = 0 if workspace is False else workspace.numel() * workspace.element_size()
-        st = lib.qgemm_int4_grouped(x.data_ptr(), _rows_ld(x, "x"), qweight.data_ptr(), scales.data_ptr(),
-                                    _ptr(qzeros), experts, offsets.data_ptr(), out.data_ptr(),
-                                    _rows_ld(out, "out"), m, n, k, group_size, wptr, wbytes, _stream(x, stream))
-    _check(st, "qgemm_int4_grouped")
+    if out is None:
+        out = x.new_empty((m, n))
+    elif out.shape != (m, n) or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bfloat16 [m][n]")
+    if workspace is None:
+        size = lib.qgemm_int4_grouped_workspace_size(experts, m, n, k)
+        if size < 0:
+            raise QGemmError(-size, "qgemm_int4_grouped_workspace_size")
+        workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else False
+    wptr, wbytes = ((None, 0) if workspace is False
+                    else (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    st = lib.qgemm_int4_grouped(x.data_ptr(), _rows_ld(x, "x"), qweight.data_ptr(), scales.data_ptr(),
+                                None if qzeros is None else qzeros.data_ptr(), experts, offsets.data_ptr(),
+                                out.data_ptr(), _rows_ld(out, "out"), m, n, k, group_size, wptr, wbytes,
+                                _raw_stream(device))
+    if st:
+        raise QGemmError(st, "qgemm_int4_grouped")
     return out
 
 
-def _dtype_name(dtype):
-    import torch
-
-    names = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
-    if dtype not in names:
+def _dtype_code(dtype):
+    code = _type_codes.get(dtype)
+    if code is None:
         raise TypeError("the dtype must be bfloat16, float16 or float32")
-    return names[dtype]
+    return code
 
 
 def _mx_matrix(codes, scales, what):
@@ -561,12 +596,11 @@ def _mx_matrix(codes, scales, what):
 
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError("%s: codes and scales must be uint8" % what)
-    if codes.dim() != 2 or scales.dim() != 2:
-        raise ValueError("%s: codes must be [rows][k/2] and scales [rows][k/32]" % what)
-    rows, k = codes.shape[0], 2 * codes.shape[1]
-    if k % 32 or tuple(scales.shape) != (rows, k // 32):
-        raise ValueError("%s: codes must be [rows][k/2] and scales [rows][k/32], k a multiple of 32" % what)
-    return rows, k
+    if codes.dim() == 2 and scales.dim() == 2:
+        rows, half = codes.shape
+        if half % 16 == 0 and scales.shape == (rows, half // 16):
+            return rows, 2 * half
+    raise ValueError("%s: codes must be [rows][k/2] and scales [rows][k/32], k a multiple of 32" % what)
 
 
 def mxfp4_quantize(x, codes=None, scales=None, stream=None):
@@ -574,73 +608,96 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     k a multiple of 32) in MXFP4: blocks of 32 along a row with one power-of-two scale, 4-bit
     e2m1 codes (see qgemm_mxfp4.h for the rounding).  New scales have rows that start on 16
     bytes (a view of padded rows when k is not a multiple of 512)."""
+    device = _device_of(x, codes, scales)
+    if _elsewhere(device, stream):
+        with _launch_on(x, stream):
+            return _mxfp4_quantize(x, codes, scales, device)
+    return _mxfp4_quantize(x, codes, scales, device)
+
+
+def _mxfp4_quantize(x, codes, scales, device):
     import torch
 
-    lib = load()
-    name = _dtype_name(x.dtype)
+    lib = _lib or load()
+    code = _dtype_code(x.dtype)
     if x.dim() != 2 or x.shape[1] % 32:
         raise ValueError("x must be [rows][k] with k a multiple of 32")
     rows, k = x.shape
-    _same_device(x, codes, scales)
-    with _launch_on(x.device, stream):
-        if codes is None:
-            codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty((rows, (k // 32 + 15) // 16 * 16), dtype=torch.uint8, device=x.device)[:, :k // 32]
-        if _mx_matrix(codes, scales, "mxfp4_quantize") != (rows, k):
-            raise ValueError("codes must be [rows][k/2] and scales [rows][k/32]")
-        st = lib.mxfp4_quantize(_DTYPES[name], rows, k, x.data_ptr(), _rows_ld(x, "x"), codes.data_ptr(),
-                                _rows_ld(codes, "codes"), scales.data_ptr(), _rows_ld(scales, "scales"),
-                                _stream(x, stream))
-    _check(st, "mxfp4_quantize")
+    if codes is None:
+        codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty((rows, (k // 32 + 15) // 16 * 16), dtype=torch.uint8)
+        if k % 512:
+            scales = scales[:, :k // 32]
+    if _mx_matrix(codes, scales, "mxfp4_quantize") != (rows, k):
+        raise ValueError("codes must be [rows][k/2] and scales [rows][k/32]")
+    st = lib.mxfp4_quantize(code, rows, k, x.data_ptr(), _rows_ld(x, "x"), codes.data_ptr(),
+                            _rows_ld(codes, "codes"), scales.data_ptr(), _rows_ld(scales, "scales"),
+                            _raw_stream(device))
+    if st:
+        raise QGemmError(st, "mxfp4_quantize")
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, dtype=None, out=None, stream=None):
     """The values [rows][k] of an MXFP4 matrix in dtype (bfloat16 when neither it nor out is given)."""
+    device = _device_of(codes, scales, out)
+    if _elsewhere(device, stream):
+        with _launch_on(codes, stream):
+            return _mxfp4_dequantize(codes, scales, dtype, out, device)
+    return _mxfp4_dequantize(codes, scales, dtype, out, device)
+
+
+def _mxfp4_dequantize(codes, scales, dtype, out, device):
     import torch
 
-    lib = load()
+    lib = _lib or load()
     rows, k = _mx_matrix(codes, scales, "mxfp4_dequantize")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
-    name = _dtype_name(dtype)
-    _same_device(codes, scales, out)
-    with _launch_on(codes.device, stream):
-        if out is None:
-            out = torch.empty((rows, k), dtype=dtype, device=codes.device)
-        elif tuple(out.shape) != (rows, k) or out.dtype != dtype:
-            raise ValueError("out must be [rows][k] of dtype")
-        st = lib.mxfp4_dequantize(_DTYPES[name], rows, k, codes.data_ptr(), _rows_ld(codes, "codes"),
-                                  scales.data_ptr(), _rows_ld(scales, "scales"), out.data_ptr(),
-                                  _rows_ld(out, "out"), _stream(codes, stream))
-    _check(st, "mxfp4_dequantize")
+    code = _dtype_code(dtype)
+    if out is None:
+        out = codes.new_empty((rows, k), dtype=dtype)
+    elif out.shape != (rows, k) or out.dtype != dtype:
+        raise ValueError("out must be [rows][k] of dtype")
+    st = lib.mxfp4_dequantize(code, rows, k, codes.data_ptr(), _rows_ld(codes, "codes"), scales.data_ptr(),
+                              _rows_ld(scales, "scales"), out.data_ptr(), _rows_ld(out, "out"),
+                              _raw_stream(device))
+    if st:
+        raise QGemmError(st, "mxfp4_dequantize")
     return out
 
 
 def gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, dtype=None, out=None, stream=None):
     """out [M][N] = A . B^T of two MXFP4 matrices A [M][K] and B [N][K] (mxfp4_quantize's codes and
     scales), summed in fp32 and rounded once to dtype (bfloat16 when neither it nor out is given)."""
+    device = _device_of(a_codes, a_scales, b_codes, b_scales, out)
+    if _elsewhere(device, stream):
+        with _launch_on(a_codes, stream):
+            return _gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, dtype, out, device)
+    return _gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, dtype, out, device)
+
+
+def _gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, dtype, out, device):
     import torch
 
-    lib = load()
+    lib = _lib or load()
     (M, K), (N, kb) = _mx_matrix(a_codes, a_scales, "a"), _mx_matrix(b_codes, b_scales, "b")
     if K != kb:
         raise ValueError("A and B must have the same k")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
-    name = _dtype_name(dtype)
-    _same_device(a_codes, a_scales, b_codes, b_scales, out)
-    with _launch_on(a_codes.device, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
-        elif tuple(out.shape) != (M, N) or out.dtype != dtype:
-            raise ValueError("out must be [M][N] of dtype")
-        st = lib.gemm_mxfp4(_DTYPES[name], M, N, K, a_codes.data_ptr(), _rows_ld(a_codes, "a_codes"),
-                            a_scales.data_ptr(), _rows_ld(a_scales, "a_scales"), b_codes.data_ptr(),
-                            _rows_ld(b_codes, "b_codes"), b_scales.data_ptr(), _rows_ld(b_scales, "b_scales"),
-                            out.data_ptr(), _rows_ld(out, "out"), _stream(a_codes, stream))
-    _check(st, "gemm_mxfp4")
+    code = _dtype_code(dtype)
+    if out is None:
+        out = a_codes.new_empty((M, N), dtype=dtype)
+    elif out.shape != (M, N) or out.dtype != dtype:
+        raise ValueError("out must be [M][N] of dtype")
+    st = lib.gemm_mxfp4(code, M, N, K, a_codes.data_ptr(), _rows_ld(a_codes, "a_codes"), a_scales.data_ptr(),
+                        _rows_ld(a_scales, "a_scales"), b_codes.data_ptr(), _rows_ld(b_codes, "b_codes"),
+                        b_scales.data_ptr(), _rows_ld(b_scales, "b_scales"), out.data_ptr(),
+                        _rows_ld(out, "out"), _raw_stream(device))
+    if st:
+        raise QGemmError(st, "gemm_mxfp4")
     return out
 
 

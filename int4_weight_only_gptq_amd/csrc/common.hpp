@@ -195,13 +195,74 @@ __device__ __forceinline__ void wait_vmcnt(int n) {
   }
 }
 
-// 16 zero bytes: what a direct load takes for a chunk past the end of k.
-__device__ const u32x4 kZeroChunk = {0u, 0u, 0u, 0u};
-
 // Slot of 16-byte chunk c (8 bf16 of k) of row r in a K-contiguous LDS tile of
 // 8 chunks per row: the XOR spreads the 16 rows one MFMA operand read touches
 // over distinct banks.
 __device__ __forceinline__ int swz(int r, int c) { return 8 * r + (c ^ (r & 7)); }
+
+// Chunk XOR of k-row k in an LDS tile that keeps its memory orientation (rows = k,
+// 16-byte chunks of 8 columns), for transposing reads: the 16 rows one such read
+// touches fall two to a bank slot, the minimum for 512 bytes.
+__device__ __forceinline__ int fmn(int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); }
+// the same XOR limited to a row of R / 8 chunks (R = 64: 8 chunks)
+template <int R>
+__device__ __forceinline__ int fmn_r(int k) { return fmn(k) & (R / 8 - 1); }
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
+
+// N (2 or 4) operand fragments of 8 consecutive k of a column from an LDS tile in its
+// memory orientation, each by two transposing reads 4 k-rows (HI bytes) apart at LDS byte
+// address at[i], complete on return.
+//
+// In asm with its wait, because the compiler puts a wait for every direct
+// global->LDS load in flight before the builtin of this read (it cannot tell their
+// addresses apart), which would undo the loads' pipelining.  Only the LDS counter is
+// waited for here.  The outputs are early-clobbered: a read that lands must not
+// overwrite an address that a later one still needs.
+template <int N, int HI>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[N], u32x4 (&out)[N]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  static_assert(N == 2 || N == 4, "fragments");
+  u32x2 lo[N], hi[N];
+  if constexpr (N == 4) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %2, %9\n\t"
+        "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %4, %10\n\t"
+        "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %6, %11\n\t"
+        "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(HI)
+        : "memory");
+  } else {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\t"
+        "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %2, %5\n\t"
+        "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1])
+        : "v"(at[0]), "v"(at[1]), "n"(HI)
+        : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = u32x4{lo[i][0], lo[i][1], hi[i][0], hi[i][1]};
+#endif
+}
+
+// LDS byte address of a pointer into shared memory.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+#else
+  return 0;
+#endif
+}
 
 // One ticket of a k split's counter (agent scope); returns the count before.
 // acq_rel != 0: an acquire-release increment (the memory model orders the
@@ -235,6 +296,27 @@ __device__ __forceinline__ void buffer_to_lds16(const void* base, uint32_t voff,
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, -1, 0x00020000),
                                            (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+#endif
+}
+
+// The same for 16 bytes over 2^31 bytes from base: lanes whose offset is kOutside read
+// nothing and fill their slot with zeros (the resource's bounds check).
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ void buffer_to_lds16_or_zero(const void* base, uint32_t voff, void* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)kOutside, 0x00020000),
+      (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+#endif
+}
+
+// 16 bytes per lane stored through the same kind of resource: lanes whose offset is
+// kOutside store nothing.  Every lane takes part, so the number of stores a wave has
+// in flight is known.
+__device__ __forceinline__ void buffer_store16_or_none(void* base, uint32_t voff, u32x4 v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_buffer_store_b128(
+      v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)kOutside, 0x00020000), voff, 0, 0);
 #endif
 }
 

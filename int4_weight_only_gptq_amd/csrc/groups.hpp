@@ -35,67 +35,89 @@ __device__ __forceinline__ int group_rows(const int32_t* offsets, int e, int row
 }
 
 struct GroupTile {
-  int group;    // -1: no tile left for this workgroup
+  int group;    // -1: none
   int row0;     // first row of the group
   int rows;     // rows of the group
   int tm, tn;   // row tile within the group, column tile
 };
 
-// Tile of workgroup `block` among every group's ceil(rows / bm) x tiles_n tiles.
-// The tiles are numbered group by group and dealt out so that each XCD (block
-// mod 8) gets one contiguous run of them; within a group they go in bands of
-// `band` row tiles, column by column, so that the about 32 tiles an XCD works on
-// at a time share row and column panels in its L2.
+// All groups' ceil(rows / bm) x tiles_n tiles, numbered group by group; within a
+// group in bands of `band` row tiles, column by column, so that tiles worked on at
+// the same time share row and column panels in an XCD's L2.
+struct GroupTiles {
+  const int32_t* offsets;
+  int groups, rows, bm, tiles_n, band, lane;
+  int lo0 = 0, rows0 = 0, sum0 = 0;     // this lane's group among the first 64
+  int64_t tiles;            // of all groups
+
+  __device__ __forceinline__ GroupTiles(const int32_t* offsets_, int groups_, int rows_, int bm_, int tiles_n_,
+                                        int band_, int lane_)
+      : offsets(offsets_), groups(groups_), rows(rows_), bm(bm_), tiles_n(tiles_n_), band(band_), lane(lane_) {
+    int row_tiles = 0;
+    for (int c = 0; c < groups; c += 64) {
+      int lo, r, sum;
+      chunk(c, lo, r, sum);
+      if (c == 0) {
+        lo0 = lo;
+        rows0 = r;
+        sum0 = sum;
+      }
+      row_tiles += __builtin_amdgcn_readlane(sum, 63);
+    }
+    tiles = (int64_t)row_tiles * tiles_n;
+  }
+
+  // groups c .. c + 63, one a lane: first row, rows, inclusive sum of row tiles
+  __device__ __forceinline__ void chunk(int c, int& lo, int& r, int& sum) const {
+    lo = 0;
+    r = c + lane < groups ? group_rows(offsets, c + lane, rows, &lo) : 0;
+    sum = wave_prefix_sum((r + bm - 1) / bm);
+  }
+
+  // Rows and first row of one group (wave-uniform e).
+  __device__ __forceinline__ int rows_of(int e, int* lo) const {
+    if (e < 64) {
+      *lo = __builtin_amdgcn_readlane(lo0, e);
+      return __builtin_amdgcn_readlane(rows0, e);
+    }
+    return group_rows(offsets, e, rows, lo);
+  }
+
+  // Tile i of XCD x: each of the 8 XCDs has one contiguous run of the tiles.
+  __device__ __forceinline__ GroupTile find(int x, int64_t i) const {
+    GroupTile g{-1, 0, 0, 0, 0};
+    const int64_t per_xcd = (tiles + 7) >> 3, item = x * per_xcd + i;
+    if (i >= per_xcd || item >= tiles) return g;
+    const int q = (int)(item / tiles_n);   // row tiles before it, over all groups
+    int base = 0;
+    for (int c = 0; c < groups; c += 64) {
+      int lo = lo0, r = rows0, sum = sum0;
+      if (c > 0) chunk(c, lo, r, sum);
+      const int total = __builtin_amdgcn_readlane(sum, 63);
+      if (q < base + total) {
+        const int l = __popcll(__ballot(base + sum <= q));   // the first lane whose sum exceeds q
+        g.group = c + l;
+        g.row0 = __builtin_amdgcn_readlane(lo, l);
+        g.rows = __builtin_amdgcn_readlane(r, l);
+        const int rt = (g.rows + bm - 1) / bm;
+        const int start = base + __builtin_amdgcn_readlane(sum, l) - rt;
+        const int local = (int)(item - (int64_t)start * tiles_n);
+        const int b = local / (band * tiles_n), in = local - b * band * tiles_n;
+        const int height = min(band, rt - b * band);
+        g.tn = in / height;
+        g.tm = b * band + (in - g.tn * height);
+        return g;
+      }
+      base += total;
+    }
+    return g;
+  }
+};
+
+// Tile of a workgroup that takes one.
 __device__ __forceinline__ GroupTile find_group_tile(const int32_t* __restrict__ offsets, int groups, int rows,
                                                      int bm, int tiles_n, int band, int block, int lane) {
-  int first_lo = 0, first_rows = 0, first_sum = 0, row_tiles = 0;
-  for (int c = 0; c < groups; c += 64) {
-    const int e = c + lane;
-    int lo = 0;
-    const int r = e < groups ? group_rows(offsets, e, rows, &lo) : 0;
-    const int sum = wave_prefix_sum((r + bm - 1) / bm);
-    if (c == 0) {
-      first_lo = lo;
-      first_rows = r;
-      first_sum = sum;
-    }
-    row_tiles += __builtin_amdgcn_readlane(sum, 63);
-  }
-  GroupTile g{-1, 0, 0, 0, 0};
-  const int64_t tiles = (int64_t)row_tiles * tiles_n;
-  const int64_t per_xcd = (tiles + 7) >> 3;
-  const int64_t item = (int64_t)(block & 7) * per_xcd + (block >> 3);
-  if ((block >> 3) >= per_xcd || item >= tiles) return g;
-  const int q = (int)(item / tiles_n);   // row tiles before it, over all groups
-  int base = 0;
-  for (int c = 0; c < groups; c += 64) {
-    int lo = first_lo, r = first_rows, sum = first_sum;
-    if (c > 0) {
-      const int e = c + lane;
-      lo = 0;
-      r = e < groups ? group_rows(offsets, e, rows, &lo) : 0;
-      sum = wave_prefix_sum((r + bm - 1) / bm);
-    }
-    const int total = __builtin_amdgcn_readlane(sum, 63);
-    if (q < base + total) {
-      // the first lane whose inclusive sum exceeds q
-      const uint64_t before = __ballot(base + sum <= q);
-      const int l = __popcll(before);
-      g.group = c + l;
-      g.row0 = __builtin_amdgcn_readlane(lo, l);
-      g.rows = __builtin_amdgcn_readlane(r, l);
-      const int rt = (g.rows + bm - 1) / bm;
-      const int start = base + __builtin_amdgcn_readlane(sum, l) - rt;
-      const int local = (int)(item - (int64_t)start * tiles_n);
-      const int b = local / (band * tiles_n), in = local - b * band * tiles_n;
-      const int height = min(band, rt - b * band);
-      g.tn = in / height;
-      g.tm = b * band + (in - g.tn * height);
-      return g;
-    }
-    base += total;
-  }
-  return g;
+  return GroupTiles(offsets, groups, rows, bm, tiles_n, band, lane).find(block & 7, block >> 3);
 }
 
 // Workgroups that cover every distribution of `rows` rows over `groups` groups

@@ -243,12 +243,14 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
 // product, many rows: BM x BN tiles
 //
 // NWV waves as a WGM x (NWV / WGM) grid, FM x FN matrix tiles of 32 x 32 each.  k
-// tiles of 256 (8 blocks, 128 bytes a row) in a ring of STAGES LDS buffers filled by
-// direct loads, chunk c of row r in slot 8 r + (c ^ (r & 7)) (conflict-free operand
-// reads).  Lane (r, h) of a 32x32x64 step s takes block 4 h + s of row r, so that its
-// four scales of a k tile are one dword.  Scales are staged 512 k at a time, 16 bytes
-// a row, through registers into two LDS buffers: the next ones are loaded at the start
-// of a pair of k tiles and written before its last barrier.
+// tiles of KB blocks (32 KB elements, 16 KB bytes a row) in a ring of STAGES LDS
+// buffers filled by direct loads, 16-byte chunk c of row r in slot KB r + (c ^ x(r))
+// with x(r) such that the rows LDS serves together fall on different banks.  Lane
+// (r, h) of 32x32x64 step s takes block h KB / 2 + s of row r, so that its scales of a
+// k tile are adjacent bytes.  Scales are staged 16 blocks (512 k) at a time, 16 bytes a
+// row, through registers into two LDS buffers of four planes (dword j of every row side
+// by side, so that their reads share no bank): the next ones are loaded in the first of
+// those k tiles and written before the last one's barrier.
 //
 // One barrier a k tile, before its last step: by then every operand of the tile is
 // in registers and the next tile has landed, so its buffer is refilled at once.
@@ -266,9 +268,9 @@ __device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int kb, int b
   return s;
 }
 
-template <int BM, int BN, int STAGES>
+template <int BM, int BN, int KB, int STAGES>
 struct MxTile {
-  static constexpr int kStage = (BM + BN) * 8;                  // 16-byte chunks
+  static constexpr int kStage = (BM + BN) * KB;                 // 16-byte chunks
   static constexpr int kScales = BM + BN;                       // 16-byte chunks per buffer
   static constexpr size_t bytes(int esize) {
     const size_t main_bytes = (size_t)(STAGES * kStage + 2 * kScales) * 16, out = (size_t)BM * (BN + 8) * 2;
@@ -276,15 +278,17 @@ struct MxTile {
   }
 };
 
-template <int BM, int BN, int STAGES, int NWV, int WGM, int DTYPE>
+template <int BM, int BN, int KB, int STAGES, int NWV, int WGM, int DTYPE>
 __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int tiles_m, int tiles_n, int per_xcd,
                                                               int a_align, int b_align, int vec) {
   constexpr int T = 64 * NWV, WM = BM / WGM, WN = BN / (NWV / WGM), FM = WM / 32, FN = WN / 32;
-  using S = MxTile<BM, BN, STAGES>;
-  constexpr int LOADS = S::kStage / T, A_LOADS = BM * 8 / T;
-  static_assert(BM * 8 % T == 0 && BN * 8 % T == 0 && BM + BN <= T && LOADS * (STAGES - 1) <= 63, "loads");
+  constexpr int STEPS = KB / 2, PER = 16 / KB;                   // steps of a k tile; k tiles of a scale buffer
+  using S = MxTile<BM, BN, KB, STAGES>;
+  constexpr int LOADS = S::kStage / T, A_LOADS = BM * KB / T;
+  constexpr int SROWS = (BM + BN + T - 1) / T;                   // rows of scales a thread stages
+  static_assert((KB == 4 || KB == 8) && BM * KB % T == 0 && BN * KB % T == 0 && LOADS * (STAGES - 1) <= 63, "loads");
   extern __shared__ __attribute__((aligned(16))) u32x4 msm[];
-  u32x4* ssm = msm + STAGES * S::kStage;                        // scales [2][BM + BN]
+  uint32_t* ssm = reinterpret_cast<uint32_t*>(msm + STAGES * S::kStage);   // scales [2][4][BM + BN]
 
   // tile order: each XCD a contiguous run; bands of kMxBand row tiles, column by column
   const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
@@ -297,30 +301,50 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
   const int r = lane & 31, h = lane >> 5;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int wm0 = (wave % WGM) * WM, wn0 = (wave / WGM) * WN;
-  const int blocks = (int)(g.K >> 5), ktiles = (blocks + 7) >> 3;
+  const int blocks = (int)(g.K >> 5), ktiles = (blocks + KB - 1) / KB;
 
-  // chunk tid + T j of a stage: row (tid + T j) / 8 of the tile's A rows then B rows
+  // chunk tid + T j of a stage: row (tid + T j) / KB of the tile's A rows then B rows
   // (rows past M or N repeat the last one), its k chunk the same for every j
-  const int chunk = (tid & 7) ^ ((tid >> 3) & 7);
-  const uint8_t* src[LOADS];
+  auto swizzle = [](int row, int c) { return KB == 8 ? c ^ (row & 7) : c ^ ((row >> 2) & 3); };
+  static_assert(T / KB % 16 == 0, "one k chunk per thread");
+  const int chunk = swizzle(tid / KB, tid % KB);
+  const uint8_t *abase = g.a + m0 * g.lda, *bbase = g.b + n0 * g.ldb;
+  uint32_t off[LOADS];      // (leading dimensions are at most 2^22 bytes)
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) {
-    const int row = (tid + T * j) >> 3;
-    src[j] = (j < A_LOADS ? g.a + min(m0 + row, g.M - 1) * g.lda : g.b + min(n0 + row - BM, g.N - 1) * g.ldb) + 16 * chunk;
+    const int row = (tid + T * j) / KB;
+    off[j] = (j < A_LOADS ? (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)g.lda
+                          : (uint32_t)min((int64_t)row - BM, g.N - 1 - n0) * (uint32_t)g.ldb) + 16 * chunk;
   }
   auto issue = [&](int kt) {
     u32x4* base = msm + (kt % STAGES) * S::kStage + 64 * wave;
-    const bool in = 8 * kt + chunk < blocks;
+    const bool in = KB * kt + chunk < blocks;    // else zeros: codes of 0
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const void* p = in ? (const void*)(src[j] + (int64_t)kt * 128) : (const void*)&kZeroChunk;
-      __builtin_amdgcn_global_load_lds((void*)p, (void*)(base + T * j), 16, 0, 0);
-    }
+    for (int j = 0; j < LOADS; ++j)
+      buffer_to_lds16_or_zero((j < A_LOADS ? abase : bbase) + (int64_t)kt * 16 * KB, in ? off[j] : kOutside,
+                              base + T * j);
   };
-  // this thread's row of scales
-  const bool srow_a = tid < BM, srow = tid < BM + BN;
-  const uint8_t* sp = srow_a ? g.as + min(m0 + tid, g.M - 1) * g.ldas : g.bs + min(n0 + tid - BM, g.N - 1) * g.ldbs;
-  const int salign = srow_a ? a_align : b_align;
+  // rows tid + T i of scales, A's then B's
+  const uint8_t* sp[SROWS];
+#pragma unroll
+  for (int i = 0; i < SROWS; ++i) {
+    const int row = tid + T * i;
+    sp[i] = row < BM ? g.as + min(m0 + row, g.M - 1) * g.ldas : g.bs + min(n0 + row - BM, g.N - 1) * g.ldbs;
+  }
+  u32x4 staged[SROWS];
+  auto load_scales = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < SROWS; ++i)
+      if (tid + T * i < BM + BN) staged[i] = load_scales16(sp[i], kb, blocks, tid + T * i < BM ? a_align : b_align);
+  };
+  auto store_scales = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < SROWS; ++i)
+      if (tid + T * i < BM + BN) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ssm[(4 * buf + j) * S::kScales + tid + T * i] = staged[i][j];
+      }
+  };
 
   f32x16 acc[FM][FN];
 #pragma unroll
@@ -334,21 +358,26 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
     u32x4 a[FM], b[FN];
   };
   auto read = [&](int kt, int s, Frags& x) {
-    const u32x4* la = msm + (kt % STAGES) * S::kStage;
+    const u32x4* la = msm + (kt % STAGES) * S::kStage + KB * r + swizzle(r, STEPS * h + s);
 #pragma unroll
-    for (int f = 0; f < FM; ++f) x.a[f] = la[swz(wm0 + 32 * f + r, 4 * h + s)];
+    for (int f = 0; f < FM; ++f) x.a[f] = la[KB * (wm0 + 32 * f)];
 #pragma unroll
-    for (int c = 0; c < FN; ++c) x.b[c] = la[swz(BM + wn0 + 32 * c + r, 4 * h + s)];
+    for (int c = 0; c < FN; ++c) x.b[c] = la[KB * (BM + wn0 + 32 * c)];
   };
   struct Scales {
     uint32_t a[FM], b[FN];
   };
   auto read_scales = [&](int kt, Scales& x) {
-    const uint32_t* l = reinterpret_cast<const uint32_t*>(ssm + ((kt >> 1) & 1) * S::kScales) + 2 * (kt & 1) + h;
+    // (dword kt % PER of the row, this lane half's two bytes; KB == 8: dword 2 (kt % PER) + h)
+    const uint32_t* l = ssm + (kt / PER % 2 * 4 + (KB == 8 ? 2 * (kt % PER) + h : kt % PER)) * S::kScales + r;
+    auto one = [&](int row) -> uint32_t {
+      if constexpr (KB == 8) return l[row];
+      else return reinterpret_cast<const uint16_t*>(l + row)[h];
+    };
 #pragma unroll
-    for (int f = 0; f < FM; ++f) x.a[f] = l[4 * (wm0 + 32 * f + r)];
+    for (int f = 0; f < FM; ++f) x.a[f] = one(wm0 + 32 * f);
 #pragma unroll
-    for (int c = 0; c < FN; ++c) x.b[c] = l[4 * (BM + wn0 + 32 * c + r)];
+    for (int c = 0; c < FN; ++c) x.b[c] = one(BM + wn0 + 32 * c);
   };
   auto multiply = [&](auto s_, const Frags& x, const Scales& sc) {
     constexpr int s = decltype(s_)::value;
@@ -363,37 +392,51 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
 #pragma unroll
   for (int st = 0; st < STAGES; ++st)
     if (st < ktiles) issue(st);
-  if (srow) ssm[tid] = load_scales16(sp, 0, blocks, salign);
+  load_scales(0);
+  store_scales(0);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  Frags x0, x1;
+  Frags x[2];
   Scales sc, next_sc;
-  read(0, 0, x0);
+  read(0, 0, x[0]);
   read_scales(0, sc);
-  u32x4 staged = {0u, 0u, 0u, 0u};
-  for (int kt = 0; kt < ktiles; ++kt) {
-    if ((kt & 1) == 0 && srow && kt + 2 < ktiles) staged = load_scales16(sp, 8 * (kt + 2), blocks, salign);
-    read(kt, 1, x1);
-    multiply(std::integral_constant<int, 0>{}, x0, sc);
-    read(kt, 2, x0);
-    multiply(std::integral_constant<int, 1>{}, x1, sc);
-    read(kt, 3, x1);
-    multiply(std::integral_constant<int, 2>{}, x0, sc);
-    if (kt + 1 < ktiles) {
-      if ((kt & 1) && srow) ssm[(((kt + 1) >> 1) & 1) * S::kScales + tid] = staged;
+  // one k tile; refill = kt + STAGES < ktiles, next = kt + 1 < ktiles (compile time)
+  auto tile = [&](int kt, auto refill, auto next) {
+    if (kt % PER == 0 && kt + PER < ktiles) load_scales(KB * (kt + PER));
+    auto step = [&](auto s_) {
+      constexpr int s = decltype(s_)::value;
+      read(kt, s + 1, x[(s + 1) & 1]);
+      multiply(s_, x[s & 1], sc);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    step(std::integral_constant<int, 0>{});
+    if constexpr (STEPS == 4) {
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+    }
+    if constexpr (decltype(next)::value) {
+      if (kt % PER == PER - 1) store_scales((kt + 1) / PER % 2);
       // this wave's reads of stage kt, its scales' write and its loads of stage kt + 1
       // are complete (the empty asm keeps the write above the wait)
       asm volatile("" ::: "memory");
-      if (kt + STAGES - 1 < ktiles) __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (STAGES - 2)) & ~(0xF << 8));
+      if constexpr (decltype(refill)::value) __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (STAGES - 2)) & ~(0xF << 8));
       else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0) & ~(0xF << 8));
       lds_barrier();
-      if (kt + STAGES < ktiles) issue(kt + STAGES);
-      read(kt + 1, 0, x0);
+      if constexpr (decltype(refill)::value) issue(kt + STAGES);
+      read(kt + 1, 0, x[0]);
       read_scales(kt + 1, next_sc);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    multiply(std::integral_constant<int, 3>{}, x1, sc);
-    sc = next_sc;
-  }
+    multiply(std::integral_constant<int, STEPS - 1>{}, x[1], sc);
+    if constexpr (decltype(next)::value) sc = next_sc;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using T_ = std::true_type;
+  using F_ = std::false_type;
+  int kt = 0;
+  for (; kt + STAGES < ktiles; ++kt) tile(kt, T_{}, T_{});
+  for (; kt + 1 < ktiles; ++kt) tile(kt, F_{}, T_{});
+  tile(kt, F_{}, F_{});
 
   // lane (r, h) holds column r and rows 8 (v / 4) + 4 h + v % 4 of each 32 x 32 block
   using O = out_t<DTYPE>;
@@ -510,13 +553,13 @@ int64_t mxfp4_threads(const MxGemmArgs& g) {
   return (p.tiles_m * p.tiles_n + 7) / 8 * 8 * p.threads;
 }
 
-template <int BM, int BN, int STAGES, int NWV, int WGM, int DTYPE>
+template <int BM, int BN, int KB, int STAGES, int NWV, int WGM, int DTYPE>
 static void mx_tile_launch(const MxGemmArgs& g, const MxPlan& p, hipStream_t stream) {
-  constexpr size_t lds = MxTile<BM, BN, STAGES>::bytes(sizeof(out_t<DTYPE>));
+  constexpr size_t lds = MxTile<BM, BN, KB, STAGES>::bytes(sizeof(out_t<DTYPE>));
   static_assert(lds <= 160 * 1024, "LDS budget");
   const int per_xcd = (int)((p.tiles_m * p.tiles_n + 7) / 8);
   const int vec = row_align(g.c, g.ldc * 2) == 16;
-  mxfp4_tile_kernel<BM, BN, STAGES, NWV, WGM, DTYPE><<<dim3((unsigned)(8 * per_xcd)), dim3(64 * NWV), lds, stream>>>(
+  mxfp4_tile_kernel<BM, BN, KB, STAGES, NWV, WGM, DTYPE><<<dim3((unsigned)(8 * per_xcd)), dim3(64 * NWV), lds, stream>>>(
       g, (int)p.tiles_m, (int)p.tiles_n, per_xcd, row_align(g.as, g.ldas), row_align(g.bs, g.ldbs), vec);
 }
 
@@ -530,11 +573,11 @@ static void mx_dispatch(const MxGemmArgs& g, hipStream_t stream) {
     if (p.bm == 16) mxfp4_strip_kernel<1, DTYPE><<<grid, block, lds, stream>>>(g, (int)p.tiles_n, ad, bd);
     else mxfp4_strip_kernel<2, DTYPE><<<grid, block, lds, stream>>>(g, (int)p.tiles_n, ad, bd);
   } else if (p.bm == 256) {
-    mx_tile_launch<256, 256, 2, 8, 2, DTYPE>(g, p, stream);
+    mx_tile_launch<256, 256, 8, 2, 8, 4, DTYPE>(g, p, stream);
   } else if (p.bm == 128) {
-    mx_tile_launch<128, 128, 4, 4, 2, DTYPE>(g, p, stream);
+    mx_tile_launch<128, 128, 8, 4, 4, 2, DTYPE>(g, p, stream);
   } else {
-    mx_tile_launch<64, 128, 4, 4, 1, DTYPE>(g, p, stream);
+    mx_tile_launch<64, 128, 8, 4, 4, 1, DTYPE>(g, p, stream);
   }
 }
 

@@ -109,7 +109,8 @@ def test_small_shapes(gpu_lib, layout, dtype):
 
 # averages that reach every kernel: strips of 16 and 32 rows, pipelined tiles of 64, 128
 # and 256 rows; k with a tail and a k longer than the strips' waves
-AVERAGES = [([1, 3, 0, 12], 5), ([20, 0, 47, 9], 1), ([64, 40, 0, 90], 1), ([100, 200, 1, 99], 1), ([500, 0, 129], 1)]
+AVERAGES = [([1, 3, 0, 12], 5), ([20, 0, 47, 9], 1), ([64, 40, 0, 90], 1), ([100, 200, 1, 99], 1), ([500, 0, 129], 1),
+            ([300, 700, 0, 1400], 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
