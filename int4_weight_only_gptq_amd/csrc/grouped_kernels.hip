@@ -6,9 +6,8 @@
 // bf16 / fp16 with fp32 accumulation, or fp32 throughout.  Three kernels:
 //  * many rows a group: pipelined MFMA tiles, a workgroup on each CU going from tile
 //    to tile;
-//  * few rows a group (decoding): the weights of the reached groups are read once
-//    and that read is the time, so a workgroup takes a strip of columns over the
-//    whole of k, split over its waves;
+//  * few rows in few groups (decoding), where the tiles would not reach every CU: a
+//    workgroup takes a strip of columns over the whole of k, split over its waves;
 //  * any alignment and size, and fp32: a tile staged through registers.
 #include "common.hpp"
 #include "groups.hpp"
@@ -366,7 +365,8 @@ __global__ __launch_bounds__(64 * NWV) void grouped_pipe_kernel(GroupedArgs a, i
 // ---------------------------------------------------------------------------
 // few rows a group: strips of columns over the whole of k
 //
-// A workgroup owns 16 RT rows of a group and a strip of columns; its waves take
+// Where the tiles would reach fewer than the 256 CUs.  A workgroup owns 16 rows of a group
+// and a strip of columns; its waves take
 // blocks of k in turn, all loads of a block issued before its MFMAs, operands
 // straight from memory into the MFMA lane layout (lane l: row or column l % 16, k
 // chunk l / 16), and the waves' partial tiles are summed through LDS in wave
@@ -378,13 +378,17 @@ __global__ __launch_bounds__(64 * NWV) void grouped_pipe_kernel(GroupedArgs a, i
 // NN, B N-contiguous: strip of 128 columns; lane (c, q) loads columns 8c .. 8c + 7
 // of the 8 k-rows 8q .. 8q + 7 and transposes the 8 x 8 block in registers:
 // fragment j then holds column 8c + j (256 contiguous bytes per k-row).
+// With enough tiles the pipelined kernel streams the weights as fast (64 rows over 64 experts,
+// 2048 -> 1024, bf16 NT 31.4 us here, 32.3 us there) and faster from a few rows a group on (512
+// rows 64.7 vs 43.9 us), since it does not load rows that are not there.
+constexpr int kStripRows = 8;     // rows a group at most, on average
 constexpr int kStripK = 256;      // k per block, NT
 constexpr int kStripKN = 32;      // k per block, NN
 
-template <int LAYOUT, int DTYPE, int RT>
+template <int LAYOUT, int DTYPE>
 __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int strips) {
   constexpr int CT = LAYOUT == 0 ? 1 : 8;               // 16-column MFMA tiles of the strip
-  constexpr int COLS = 16 * CT, ROWS = 16 * RT;
+  constexpr int COLS = 16 * CT, ROWS = 16;
   extern __shared__ __attribute__((aligned(16))) float ssm[];   // [waves][ROWS][COLS + 4]
   const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -393,70 +397,54 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
   const int cl = lane & 15, ks = lane >> 4;
   const int K = (int)a.K, N = (int)a.N;
   const int r0 = g.tm * ROWS, n0 = g.tn * COLS;
-  const uint16_t* arow[RT];
-#pragma unroll
-  for (int f = 0; f < RT; ++f)
-    arow[f] = a.A + (int64_t)(g.row0 + min(r0 + 16 * f + cl, g.rows - 1)) * a.lda;
+  const uint16_t* arow = a.A + (int64_t)(g.row0 + min(r0 + cl, g.rows - 1)) * a.lda;
   const uint16_t* B = a.B + (int64_t)g.group * a.sb;
 
-  f32x4 acc[RT][CT];
+  f32x4 acc[CT];
 #pragma unroll
-  for (int f = 0; f < RT; ++f)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[f][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 zero = {0u, 0u, 0u, 0u};
 
   if constexpr (LAYOUT == 0) {
     const uint16_t* brow = B + (int64_t)min(n0 + cl, N - 1) * a.ldb;
     for (int k0 = kStripK * wave; k0 < K; k0 += kStripK * waves) {
-      u32x4 b[8], x[RT][8];
+      u32x4 b[8], x[8];
       // past the end of k both operands are zeros (loads from the row's start)
       if (k0 + kStripK <= K) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) b[s] = *reinterpret_cast<const u32x4*>(brow + k0 + 32 * s + 8 * ks);
 #pragma unroll
-        for (int f = 0; f < RT; ++f)
-#pragma unroll
-          for (int s = 0; s < 8; ++s) x[f][s] = *reinterpret_cast<const u32x4*>(arow[f] + k0 + 32 * s + 8 * ks);
+        for (int s = 0; s < 8; ++s) x[s] = *reinterpret_cast<const u32x4*>(arow + k0 + 32 * s + 8 * ks);
       } else {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const int k = k0 + 32 * s + 8 * ks;
           b[s] = *reinterpret_cast<const u32x4*>(brow + (k < K ? k : 0));
           if (k >= K) b[s] = zero;
-#pragma unroll
-          for (int f = 0; f < RT; ++f) {
-            x[f][s] = *reinterpret_cast<const u32x4*>(arow[f] + (k < K ? k : 0));
-            if (k >= K) x[f][s] = zero;
-          }
+          x[s] = *reinterpret_cast<const u32x4*>(arow + (k < K ? k : 0));
+          if (k >= K) x[s] = zero;
         }
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-#pragma unroll
-        for (int f = 0; f < RT; ++f) acc[f][0] = mfma16<DTYPE>(x[f][s], b[s], acc[f][0]);
+      for (int s = 0; s < 8; ++s) acc[0] = mfma16<DTYPE>(x[s], b[s], acc[0]);
     }
   } else {
     const int col = min(n0 + 8 * cl, N - 8);
     for (int k0 = kStripKN * wave; k0 < K; k0 += kStripKN * waves) {
-      u32x4 in[8], b[8], x[RT];
+      u32x4 in[8], b[8], x;
       const int k = k0 + 8 * ks;
       if (k0 + kStripKN <= K) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) in[i] = *reinterpret_cast<const u32x4*>(B + (int64_t)(k + i) * a.ldb + col);
-#pragma unroll
-        for (int f = 0; f < RT; ++f) x[f] = *reinterpret_cast<const u32x4*>(arow[f] + k);
+        x = *reinterpret_cast<const u32x4*>(arow + k);
       } else {   // K % 8 == 0: a lane's 8 k-rows are all inside or all outside
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           in[i] = *reinterpret_cast<const u32x4*>(B + (int64_t)(k < K ? k + i : 0) * a.ldb + col);
           if (k >= K) in[i] = zero;
         }
-#pragma unroll
-        for (int f = 0; f < RT; ++f) {
-          x[f] = *reinterpret_cast<const u32x4*>(arow[f] + (k < K ? k : 0));
-          if (k >= K) x[f] = zero;
-        }
+        x = *reinterpret_cast<const u32x4*>(arow + (k < K ? k : 0));
+        if (k >= K) x = zero;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -465,9 +453,7 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
         for (int p = 0; p < 4; ++p) b[j][p] = __builtin_amdgcn_perm(in[2 * p + 1][j >> 1], in[2 * p][j >> 1], sel);
       }
 #pragma unroll
-      for (int f = 0; f < RT; ++f)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[f][j] = mfma16<DTYPE>(x[f], b[j], acc[f][j]);
+      for (int j = 0; j < 8; ++j) acc[j] = mfma16<DTYPE>(x, b[j], acc[j]);
     }
   }
 
@@ -475,11 +461,9 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
   constexpr int P = COLS + 4;
   float* mine = ssm + wave * ROWS * P;
 #pragma unroll
-  for (int f = 0; f < RT; ++f)
+  for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) mine[(16 * f + 4 * ks + v) * P + (LAYOUT == 0 ? cl : 8 * cl + c)] = acc[f][c][v];
+    for (int v = 0; v < 4; ++v) mine[(4 * ks + v) * P + (LAYOUT == 0 ? cl : 8 * cl + c)] = acc[c][v];
   __syncthreads();
   for (int i = tid; i < ROWS * COLS; i += blockDim.x) {
     const int r = i / COLS, c = i - r * COLS;
@@ -647,10 +631,10 @@ constexpr int kCus = 256;
 // 205 us; 12000 rows over 16, 1024 -> 1024, NT 29.4 / 36.4 / 47.1 us; 3200 rows 24.6 / 18.1 /
 // 17.4 us.  Groups' last row tiles are taken as half full.
 static int pick_row_tile(int64_t rows, int64_t groups, int64_t N) {
-  int best = 256;
+  int best = 64;
   double best_cost = 1e300;
   for (int bm : {256, 128, 64}) {
-    if (bm / 4 > rows / groups) continue;
+    if (bm > 64 && bm / 4 > rows / groups) continue;
     const int64_t tiles = (rows / bm + (groups + 1) / 2) * (bm == 64 ? (N + 127) / 128 : (N + 255) / 256);
     const int64_t resident = bm == 64 ? 2 * kCus : kCus;
     const double cost = (double)((tiles + resident - 1) / resident) * (bm == 256 ? 1.0 : bm == 128 ? 0.78 : 0.65);
@@ -672,9 +656,9 @@ static GroupedPlan plan_grouped(const GroupedArgs& a) {
       const int64_t big = a.groups * ((a.M + 255) / 256) * ((a.N + 255) / 256);
       p = big > kCus / 2 ? GroupedPlan{GroupedPlan::kPipe, 256, 256, 512, 0}
                          : GroupedPlan{GroupedPlan::kPipe, 128, 256, 256, 0};
-    } else if (avg <= 24) {
+    } else if (avg <= kStripRows && (a.rows < a.groups ? a.rows : a.groups) * ((a.N + 127) / 128) <= kCus) {
       const int64_t k_block = a.layout == 0 ? kStripK : kStripKN, waves = (a.K + k_block - 1) / k_block;
-      p = {GroupedPlan::kStrip, avg <= 8 ? 16 : 32, a.layout == 0 ? 16 : 128, (int)(64 * (waves < 8 ? waves : 8)), 0};
+      p = {GroupedPlan::kStrip, 16, a.layout == 0 ? 16 : 128, (int)(64 * (waves < 8 ? waves : 8)), 0};
     } else {
       const int bm = pick_row_tile(a.rows, a.groups, a.N);
       p = {GroupedPlan::kPipe, bm, bm == 64 ? 128 : 256, bm == 64 ? 256 : 512, 0};
@@ -707,10 +691,10 @@ static void pipe_launch(const GroupedArgs& a, const GroupedPlan& p, hipStream_t 
       a, LAYOUT == 2 ? (int)((a.M + BM - 1) / BM) : 0, (int)((a.N + BN - 1) / BN), vec);
 }
 
-template <int LAYOUT, int DTYPE, int RT>
+template <int LAYOUT, int DTYPE>
 static void strip_launch(const GroupedArgs& a, const GroupedPlan& p, hipStream_t stream) {
-  const size_t lds = (size_t)(p.threads / 64) * 16 * RT * (p.bn + 4) * 4;
-  grouped_strip_kernel<LAYOUT, DTYPE, RT><<<dim3((unsigned)p.blocks), dim3((unsigned)p.threads), lds, stream>>>(
+  const size_t lds = (size_t)(p.threads / 64) * 16 * (p.bn + 4) * 4;
+  grouped_strip_kernel<LAYOUT, DTYPE><<<dim3((unsigned)p.blocks), dim3((unsigned)p.threads), lds, stream>>>(
       a, (int)((a.N + p.bn - 1) / p.bn));
 }
 
@@ -729,8 +713,7 @@ static void dispatch16(const GroupedArgs& a, const GroupedPlan& p, hipStream_t s
     if (p.bm == 128) pipe_launch<LAYOUT, DTYPE, 128, 256, 3, 4, 1>(a, p, stream);
     else pipe_launch<LAYOUT, DTYPE, 256, 256, 4, 8, 2>(a, p, stream);
   } else if (p.kind == GroupedPlan::kStrip) {
-    if (p.bm == 16) strip_launch<LAYOUT, DTYPE, 1>(a, p, stream);
-    else strip_launch<LAYOUT, DTYPE, 2>(a, p, stream);
+    strip_launch<LAYOUT, DTYPE>(a, p, stream);
   } else {
     if (p.bm == 64) pipe_launch<LAYOUT, DTYPE, 64, 128, 6, 4, 1>(a, p, stream);
     else if (p.bm == 128) pipe_launch<LAYOUT, DTYPE, 128, 256, 5, 8, 2>(a, p, stream);
