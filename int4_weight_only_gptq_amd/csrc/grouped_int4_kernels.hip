@@ -27,12 +27,14 @@ constexpr int kInt4Band = 8;   // row tiles per band of an expert's tile order
 // k groups w, w + waves, ...  Lane (cl, ks) loads CPL adjacent words of word row
 // 4 s + ks: fragment c of step s then holds column CPL cl + c, and a word row's
 // 16 lanes read 64 CPL contiguous bytes.  Both operands go from memory into the
-// MFMA lane layout; the activations come from L2 (rows past the expert's end repeat
-// its last row: the same cache lines).  kInFlight groups are loaded before the
-// first is multiplied.  The waves' partial tiles are summed through LDS in wave
-// order.
+// MFMA lane layout; the activations come from L2, only by the lanes whose rows there
+// are (an expert has a few of the 16: 64 rows over 16 experts, 4096 -> 14336, 126 -> 95 us,
+// the time of the weights at a large copy's rate).  One group a wave at a time, so
+// that four workgroups share a CU and hide each other's latency (two at a time, half
+// as many: 119 us).  Strips of 64 columns where that gives two workgroups a CU, else
+// 32 or 16 (32 at the size above: 192 us).  The waves' partial tiles are summed
+// through LDS in wave order.
 // ---------------------------------------------------------------------------
-constexpr int kInFlight = 2;
 
 template <int RT, int CPL>
 __global__ __launch_bounds__(512) void grouped_int4_strip_kernel(Int4GroupedArgs a, int strips) {
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(512) void grouped_int4_strip_kernel(Int4GroupedArgs
   const int zshift = 4 * (col & 7);
   const uint16_t* xr[RT];
 #pragma unroll
-  for (int f = 0; f < RT; ++f) xr[f] = a.x + (int64_t)(t.row0 + min(r0 + 16 * f + cl, t.rows - 1)) * a.ldx;
+  for (int f = 0; f < RT; ++f) xr[f] = a.x + (int64_t)(t.row0 + r0 + 16 * f + cl) * a.ldx;   // (read below t.rows)
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = {kOnesBf16x2, kOnesBf16x2, kOnesBf16x2, kOnesBf16x2};
@@ -65,39 +67,37 @@ __global__ __launch_bounds__(512) void grouped_int4_strip_kernel(Int4GroupedArgs
 #pragma unroll
     for (int c = 0; c < CPL; ++c) total[f][c] = zero;
 
-  struct Regs {
-    uint32_t w[4][CPL];
+  for (int g = wave; g < groups; g += waves) {
+    uint32_t words[4][CPL];
     u32x4 x[RT][4];
-    Meta<CPL> meta;
-  } reg[kInFlight];
-  auto load = [&](int g, Regs& r) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      load_words<CPL>(qp + (int64_t)(16 * g + 4 * s + ks) * n, r.w[s]);
+      load_words<CPL>(qp + (int64_t)(16 * g + 4 * s + ks) * n, words[s]);
 #pragma unroll
-      for (int f = 0; f < RT; ++f) r.x[f][s] = *reinterpret_cast<const u32x4*>(xr[f] + 128 * g + 32 * s + 8 * ks);
+      for (int f = 0; f < RT; ++f) {
+        x[f][s] = u32x4{0u, 0u, 0u, 0u};
+        if (r0 + 16 * f + cl < t.rows) x[f][s] = *reinterpret_cast<const u32x4*>(xr[f] + 128 * g + 32 * s + 8 * ks);
+      }
     }
-    r.meta = load_meta<CPL>(sp + (int64_t)g * n, zp + g * zstride);
-  };
-  auto multiply = [&](const Regs& r) {
+    const Meta<CPL> meta = load_meta<CPL>(sp + (int64_t)g * n, zp + g * zstride);
     f32x4 acc[RT][CPL], xs[RT];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       u32x4 xp[RT];
 #pragma unroll
       for (int f = 0; f < RT; ++f) {
-        xp[f] = x_pairs_permuted(r.x[f][s]);
+        xp[f] = x_pairs_permuted(x[f][s]);
         xs[f] = mfma16_bf16(xp[f], ones, s == 0 ? zero : xs[f]);
       }
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const u32x4 w = codes_as_bf16_pairs(r.w[s][c]);
+        const u32x4 w = codes_as_bf16_pairs(words[s][c]);
 #pragma unroll
         for (int f = 0; f < RT; ++f) acc[f][c] = mfma16_bf16(xp[f], w, s == 0 ? zero : acc[f][c]);
       }
     }
     float sc[CPL], bz[CPL];
-    decode_meta<CPL>(r.meta, zshift, zmask, sc, bz);
+    decode_meta<CPL>(meta, zshift, zmask, sc, bz);
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
@@ -105,17 +105,6 @@ __global__ __launch_bounds__(512) void grouped_int4_strip_kernel(Int4GroupedArgs
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           total[f][c][v] = __builtin_fmaf(sc[c], __builtin_fmaf(-bz[c], xs[f][v], acc[f][c][v]), total[f][c][v]);
-  };
-  int g = wave;
-  for (; g + (kInFlight - 1) * waves < groups; g += kInFlight * waves) {
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) load(g + i * waves, reg[i]);
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) multiply(reg[i]);
-  }
-  for (; g < groups; g += waves) {
-    load(g, reg[0]);
-    multiply(reg[0]);
   }
 
   float* mine = ism + wave * ROWS * P;

@@ -370,8 +370,7 @@ __global__ __launch_bounds__(64 * NWV) void grouped_pipe_kernel(GroupedArgs a, i
 // blocks of k in turn, all loads of a block issued before its MFMAs, operands
 // straight from memory into the MFMA lane layout (lane l: row or column l % 16, k
 // chunk l / 16), and the waves' partial tiles are summed through LDS in wave
-// order.  The activations are read from L2 (rows past the group's end repeat
-// its last row: the same cache lines).
+// order.  The activations are read from L2, only by the lanes whose rows there are.
 // ---------------------------------------------------------------------------
 // NT, B K-contiguous: strip of 16 columns, blocks of 256 k, so a column's 512
 // contiguous bytes are read by one wave.
@@ -414,7 +413,11 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
 #pragma unroll
         for (int s = 0; s < 8; ++s) b[s] = *reinterpret_cast<const u32x4*>(brow + k0 + 32 * s + 8 * ks);
 #pragma unroll
-        for (int s = 0; s < 8; ++s) x[s] = *reinterpret_cast<const u32x4*>(arow + k0 + 32 * s + 8 * ks);
+        for (int s = 0; s < 8; ++s) x[s] = zero;
+        if (r0 + cl < g.rows) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s) x[s] = *reinterpret_cast<const u32x4*>(arow + k0 + 32 * s + 8 * ks);
+        }
       } else {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
@@ -436,7 +439,8 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
       if (k0 + kStripKN <= K) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) in[i] = *reinterpret_cast<const u32x4*>(B + (int64_t)(k + i) * a.ldb + col);
-        x = *reinterpret_cast<const u32x4*>(arow + k);
+        x = zero;
+        if (r0 + cl < g.rows) x = *reinterpret_cast<const u32x4*>(arow + k);
       } else {   // K % 8 == 0: a lane's 8 k-rows are all inside or all outside
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -475,20 +479,25 @@ __global__ __launch_bounds__(512) void grouped_strip_kernel(GroupedArgs a, int s
 }
 
 // ---------------------------------------------------------------------------
-// any alignment, fp32: a 64 x 64 tile staged through registers
+// any alignment, fp32: BM x 64 tiles staged through registers
 //
-// 4 waves (2 x 2, 32 x 32 each), k tiles of 32 in two LDS buffers, elements
-// loaded one by one along the operand's contiguous direction (guarded: zeros
-// past M, N and k, so nothing outside the matrices is read).  Both operands are
-// K-contiguous in LDS.
+// 4 waves (2 x 2, BM / 2 x 32 each), k tiles of 32 in two LDS buffers, loads guarded:
+// zeros past M, N and k, so nothing outside the matrices is read.  Elements are
+// loaded one by one along the operand's contiguous direction and stored K-contiguous
+// in LDS; with VEC (fp32 whose rows start on 16 bytes and hold whole quadruples) four at
+// a time, kept in their memory orientation.
+//
+// fp32 is bound by the matrix cores, and then by how evenly the tiles fall on the CUs:
+// 1402 rows over 8 groups, 1000 -> 1416, take 79 us one by one with 64 rows, 70 us with VEC,
+// 64 us with VEC and 32 rows (27 us at the rate of a large library product).
 // ---------------------------------------------------------------------------
-template <int LAYOUT, typename T>
+template <int LAYOUT, typename T, int BM, bool VEC>
 __global__ __launch_bounds__(256) void grouped_tile_kernel(GroupedArgs a, int tiles_m, int tiles_n) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr bool BF = std::is_same<T, __bf16>::value;
-  constexpr int BT = 64, BK = 32, P = F32 ? BK + 4 : BK + 8;     // LDS row pitch (16-byte rows)
-  constexpr int PER = BT * BK / 256;                             // elements per thread and operand
-  __shared__ __attribute__((aligned(16))) T sm[2][2][BT * P];
+  constexpr int BN = 64, BK = 32, P = BK + 8;     // LDS row pitch (16-byte rows)
+  constexpr int FM = BM / 32;                                    // 16-row blocks of a wave
+  __shared__ __attribute__((aligned(16))) T sm[2][(BM + BN) * P];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, cl = lane & 15, ks = lane >> 4;
   const T* A = reinterpret_cast<const T*>(a.A);
   const T* B = reinterpret_cast<const T*>(a.B);
@@ -506,7 +515,7 @@ __global__ __launch_bounds__(256) void grouped_tile_kernel(GroupedArgs a, int ti
     tm = t / tiles_n;
     tn = t - tm * tiles_n;
   } else {
-    const GroupTile g = find_group_tile(a.offsets, (int)a.groups, (int)a.rows, BT, tiles_n, kBand, blockIdx.x, lane);
+    const GroupTile g = find_group_tile(a.offsets, (int)a.groups, (int)a.rows, BM, tiles_n, kBand, blockIdx.x, lane);
     if (g.group < 0) return;
     A += (int64_t)g.row0 * a.lda;
     B += (int64_t)g.group * a.sb;
@@ -516,81 +525,116 @@ __global__ __launch_bounds__(256) void grouped_tile_kernel(GroupedArgs a, int ti
     tm = g.tm;
     tn = g.tn;
   }
-  const int64_t m0 = (int64_t)tm * BT, n0 = (int64_t)tn * BT, N = a.N;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN, N = a.N;
   constexpr bool A_MN = LAYOUT == 2, B_MN = LAYOUT != 0;
 
-  // element i of a thread: K-contiguous: row tid / 32 + 8 i, k tid % 32;
-  // else: row tid % 64, k tid / 64 + 4 i
-  auto load = [&](const T* p, int64_t ld, bool mn, int64_t first, int64_t end, int64_t k0, T (&reg)[PER]) {
+  // element i of a thread: K-contiguous: row tid / 32 + 8 i, k tid % 32; else: row tid % R,
+  // k tid / R + 256 / R i.  VEC, quadruple i: row tid / 8 + 32 i, k 4 (tid % 8); else: rows from
+  // 4 (tid % (R / 4)) on, k tid / (R / 4) + 1024 / R i, in LDS k-rows of R + 4 elements.
+  auto load = [&](auto r_, const T* p, int64_t ld, bool mn, int64_t first, int64_t end, int64_t k0, auto& reg) {
+    constexpr int R = decltype(r_)::value, PER = R * BK / 256;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int64_t r = first + (mn ? tid & 63 : (tid >> 5) + 8 * i), k = k0 + (mn ? (tid >> 6) + 4 * i : tid & 31);
-      reg[i] = r < end && k < K ? (mn ? p[k * ld + r] : p[r * ld + k]) : (T)0.f;
+      for (int i = 0; i < PER / 4; ++i) {
+        const int64_t r = first + (mn ? 4 * (tid % (R / 4)) : (tid >> 3) + 32 * i);
+        const int64_t k = k0 + (mn ? tid / (R / 4) + 1024 / R * i : 4 * (tid & 7));
+        const f32x4 v = r < end && k < K ? *reinterpret_cast<const f32x4*>(p + (mn ? k * ld + r : r * ld + k))
+                                         : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reg[4 * i + j] = v[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int64_t r = first + (mn ? tid % R : (tid >> 5) + 8 * i), k = k0 + (mn ? tid / R + 256 / R * i : tid & 31);
+        reg[i] = r < end && k < K ? (mn ? p[k * ld + r] : p[r * ld + k]) : (T)0.f;
+      }
     }
   };
-  auto store = [&](T* region, bool mn, const T (&reg)[PER]) {
+  auto store = [&](auto r_, T* region, bool mn, const auto& reg) {
+    constexpr int R = decltype(r_)::value, PER = R * BK / 256;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      region[mn ? (tid & 63) * P + (tid >> 6) + 4 * i : ((tid >> 5) + 8 * i) * P + (tid & 31)] = reg[i];
+      for (int i = 0; i < PER / 4; ++i)
+        *reinterpret_cast<f32x4*>(region + (mn ? (tid / (R / 4) + 1024 / R * i) * (R + 4) + 4 * (tid % (R / 4))
+                                               : ((tid >> 3) + 32 * i) * P + 4 * (tid & 7))) =
+            f32x4{reg[4 * i], reg[4 * i + 1], reg[4 * i + 2], reg[4 * i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        region[mn ? (tid % R) * P + tid / R + 256 / R * i : ((tid >> 5) + 8 * i) * P + (tid & 31)] = reg[i];
+    }
   };
-  f32x4 acc[2][2];
+  // fp32: the k 16 q + 4 ks .. + 3 of a row (the same k of both operands)
+  auto quad = [&](auto r_, const T* region, bool mn, int row, int q) {
+    if constexpr (VEC) {
+      constexpr int PM = decltype(r_)::value + 4;
+      if (mn) {
+        const T* c = region + (16 * q + 4 * ks) * PM + row;
+        return f32x4{c[0], c[PM], c[2 * PM], c[3 * PM]};
+      }
+    }
+    return *reinterpret_cast<const f32x4*>(region + row * P + 16 * q + 4 * ks);
+  };
+  const std::integral_constant<int, BM> RA;
+  const std::integral_constant<int, BN> RB;
+  f32x4 acc[FM][2];
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int c = 0; c < 2; ++c) acc[f][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  T ra[PER], rb[PER];
+  const int wm = (wave & 1) * (BM / 2), wn = (wave >> 1) * 32;
+  T ra[BM * BK / 256], rb[BN * BK / 256];
   const int64_t ktiles = (K + BK - 1) / BK;
   if (ktiles > 0) {
-    load(A, a.lda, A_MN, m0, M, 0, ra);
-    load(B, a.ldb, B_MN, n0, N, 0, rb);
-    store(sm[0][0], A_MN, ra);
-    store(sm[0][1], B_MN, rb);
+    load(RA, A, a.lda, A_MN, m0, M, 0, ra);
+    load(RB, B, a.ldb, B_MN, n0, N, 0, rb);
+    store(RA, sm[0], A_MN, ra);
+    store(RB, sm[0] + BM * P, B_MN, rb);
   }
   __syncthreads();
   for (int64_t kt = 0; kt < ktiles; ++kt) {
     const int buf = (int)(kt & 1);
     const bool more = kt + 1 < ktiles;
     if (more) {
-      load(A, a.lda, A_MN, m0, M, (kt + 1) * BK, ra);
-      load(B, a.ldb, B_MN, n0, N, (kt + 1) * BK, rb);
+      load(RA, A, a.lda, A_MN, m0, M, (kt + 1) * BK, ra);
+      load(RB, B, a.ldb, B_MN, n0, N, (kt + 1) * BK, rb);
     }
-    const T *la = sm[buf][0], *lb = sm[buf][1];
+    const T *la = sm[buf], *lb = la + BM * P;
     if constexpr (F32) {
-      // k order within 16: lane group ks takes 4 ks .. 4 ks + 3 of both operands
 #pragma unroll
       for (int q = 0; q < BK / 16; ++q) {
-        f32x4 x[2], w[2];
+        f32x4 x[FM], w[2];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) x[f] = *reinterpret_cast<const f32x4*>(la + (wm + 16 * f + cl) * P + 16 * q + 4 * ks);
+        for (int f = 0; f < FM; ++f) x[f] = quad(RA, la, A_MN, wm + 16 * f + cl, q);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) w[c] = *reinterpret_cast<const f32x4*>(lb + (wn + 16 * c + cl) * P + 16 * q + 4 * ks);
+        for (int c = 0; c < 2; ++c) w[c] = quad(RB, lb, B_MN, wn + 16 * c + cl, q);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+          for (int f = 0; f < FM; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c) acc[f][c] = mfma16_f32(x[f][j], w[c][j], acc[f][c]);
       }
     } else {
-      u32x4 x[2], w[2];
+      u32x4 x[FM], w[2];
 #pragma unroll
-      for (int f = 0; f < 2; ++f) x[f] = *reinterpret_cast<const u32x4*>(la + (wm + 16 * f + cl) * P + 8 * ks);
+      for (int f = 0; f < FM; ++f) x[f] = *reinterpret_cast<const u32x4*>(la + (wm + 16 * f + cl) * P + 8 * ks);
 #pragma unroll
       for (int c = 0; c < 2; ++c) w[c] = *reinterpret_cast<const u32x4*>(lb + (wn + 16 * c + cl) * P + 8 * ks);
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int c = 0; c < 2; ++c) acc[f][c] = mfma16<BF ? 0 : 1>(x[f], w[c], acc[f][c]);
     }
     if (more) {
-      store(sm[buf ^ 1][0], A_MN, ra);
-      store(sm[buf ^ 1][1], B_MN, rb);
+      store(RA, sm[buf ^ 1], A_MN, ra);
+      store(RB, sm[buf ^ 1] + BM * P, B_MN, rb);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -649,7 +693,11 @@ static int pick_row_tile(int64_t rows, int64_t groups, int64_t N) {
 static GroupedPlan plan_grouped(const GroupedArgs& a) {
   GroupedPlan p{GroupedPlan::kTile, 64, 64, 256, 0};
   const int64_t avg = a.rows / a.groups;
-  if (a.dtype != 2 && a.K > 0 && vectorizable(a)) {
+  if (a.dtype == 2) {
+    // 32-row tiles while 64-row ones would be fewer than 4 a CU
+    const int64_t row_tiles = a.layout == 2 ? a.groups * ((a.M + 63) / 64) : a.rows / 64 + (a.groups + 1) / 2;
+    if (row_tiles * ((a.N + 63) / 64) < 4 * kCus) p.bm = 32;
+  } else if (a.K > 0 && vectorizable(a)) {
     if (a.layout == 2) {
       // 128 x 256 tiles (4 waves, two workgroups a CU) where 256 x 256 ones would leave
       // half of the CUs idle
@@ -698,17 +746,31 @@ static void strip_launch(const GroupedArgs& a, const GroupedPlan& p, hipStream_t
       a, (int)((a.N + p.bn - 1) / p.bn));
 }
 
-template <int LAYOUT, typename T>
+template <int LAYOUT, typename T, int BM>
 static void tile_launch(const GroupedArgs& a, const GroupedPlan& p, hipStream_t stream) {
-  grouped_tile_kernel<LAYOUT, T><<<dim3((unsigned)p.blocks), dim3(256), 0, stream>>>(
-      a, LAYOUT == 2 ? (int)((a.M + 63) / 64) : 0, (int)((a.N + 63) / 64));
+  const dim3 grid((unsigned)p.blocks);
+  const int tiles_m = LAYOUT == 2 ? (int)((a.M + BM - 1) / BM) : 0, tiles_n = (int)((a.N + 63) / 64);
+  if constexpr (sizeof(T) == 4) {
+    const int64_t a_contig = LAYOUT == 2 ? a.M : a.K, b_contig = LAYOUT == 0 ? a.K : a.N;
+    if (aligned16(a.A) && aligned16(a.B) && (a.lda | a.ldb | a.sb | a_contig | b_contig) % 4 == 0) {
+      grouped_tile_kernel<LAYOUT, T, BM, true><<<grid, dim3(256), 0, stream>>>(a, tiles_m, tiles_n);
+      return;
+    }
+  }
+  grouped_tile_kernel<LAYOUT, T, BM, false><<<grid, dim3(256), 0, stream>>>(a, tiles_m, tiles_n);
+}
+
+template <int LAYOUT>
+static void dispatch32(const GroupedArgs& a, const GroupedPlan& p, hipStream_t stream) {
+  if (p.bm == 32) tile_launch<LAYOUT, float, 32>(a, p, stream);
+  else tile_launch<LAYOUT, float, 64>(a, p, stream);
 }
 
 template <int LAYOUT, int DTYPE>
 static void dispatch16(const GroupedArgs& a, const GroupedPlan& p, hipStream_t stream) {
   using T = std::conditional_t<DTYPE == 0, __bf16, _Float16>;
   if (p.kind == GroupedPlan::kTile) {
-    tile_launch<LAYOUT, T>(a, p, stream);
+    tile_launch<LAYOUT, T, 64>(a, p, stream);
   } else if constexpr (LAYOUT == 2) {
     if (p.bm == 128) pipe_launch<LAYOUT, DTYPE, 128, 256, 3, 4, 1>(a, p, stream);
     else pipe_launch<LAYOUT, DTYPE, 256, 256, 4, 8, 2>(a, p, stream);
@@ -726,13 +788,13 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {
   switch (a.layout * 3 + a.dtype) {
     case 0: dispatch16<0, 0>(a, p, stream); break;
     case 1: dispatch16<0, 1>(a, p, stream); break;
-    case 2: tile_launch<0, float>(a, p, stream); break;
+    case 2: dispatch32<0>(a, p, stream); break;
     case 3: dispatch16<1, 0>(a, p, stream); break;
     case 4: dispatch16<1, 1>(a, p, stream); break;
-    case 5: tile_launch<1, float>(a, p, stream); break;
+    case 5: dispatch32<1>(a, p, stream); break;
     case 6: dispatch16<2, 0>(a, p, stream); break;
     case 7: dispatch16<2, 1>(a, p, stream); break;
-    case 8: tile_launch<2, float>(a, p, stream); break;
+    case 8: dispatch32<2>(a, p, stream); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -142,7 +142,8 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __
 // chunks of 512 k in turn.  Lane (r, q) holds blocks 4 q .. 4 q + 3 of row r's 16
 // blocks of a chunk: 64 contiguous bytes of codes and one dword of scales, one block
 // a 16x16x128 step (which blocks meet in a step does not matter, so long as both
-// operands agree).  A strip's read of B is the time; A comes from L2.
+// operands agree).  A strip's read of B is the time; A comes from L2, only by the lanes
+// whose rows there are.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
@@ -191,8 +192,13 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
 #pragma unroll
       for (int f = 0; f < RT; ++f) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) a[f][s] = *reinterpret_cast<const u32x4*>(ap[f] + 16 * (kb + s));
-        sa[f] = load_scales4(as[f], kb, blocks, a_dwords);
+        for (int s = 0; s < 4; ++s) a[f][s] = u32x4{0u, 0u, 0u, 0u};
+        sa[f] = kOneScales;
+        if (r0 + 16 * f + r < g.M) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) a[f][s] = *reinterpret_cast<const u32x4*>(ap[f] + 16 * (kb + s));
+          sa[f] = load_scales4(as[f], kb, blocks, a_dwords);
+        }
       }
     } else {   // past the end of k: codes of zero, scales of one
 #pragma unroll
