@@ -10,7 +10,7 @@
  *           sign, bits 2..0 one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.  16-byte aligned,
  *           ld % 16 == 0, ld <= 2^22.
  *   scales  uint8 [rows][ld], ld >= k / 32: byte b of a row stands for 2^(byte - 127)
- *           (0 .. 254); 255 is NaN, and makes its whole block NaN.  Any alignment;
+ *           (0 .. 254); 255 is NaN, and makes its whole block NaN.  ld <= 2^22, any alignment;
  *           rows that start on 16 bytes (4 bytes) are read fastest (faster).
  * An element's value is code * scale.
  */

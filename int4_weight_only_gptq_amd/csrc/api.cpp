@@ -447,7 +447,7 @@ static int32_t check_mxfp4(int64_t k, const uint8_t* codes, int64_t ld_codes, co
                            int64_t ld_scales) {
   if (codes == nullptr || scales == nullptr) return QG_ERR_NULL;
   if (ld_codes < k / 2 || ld_scales < k / 32) return QG_ERR_SHAPE;
-  if (ld_codes > (int64_t)1 << 22) return QG_ERR_SHAPE;   // a tile's rows are addressed in 31 bits
+  if (ld_codes > (int64_t)1 << 22 || ld_scales > (int64_t)1 << 22) return QG_ERR_SHAPE;   // a tile's rows take 31 bits
   if (!aligned(codes, 16) || ld_codes % 16 != 0) return QG_ERR_ALIGN;
   return QG_OK;
 }

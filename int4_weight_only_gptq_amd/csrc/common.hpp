@@ -339,6 +339,16 @@ __device__ __forceinline__ u32x4 buffer_load16(const void* base, uint32_t voff) 
 #endif
 }
 
+// buffer_load16 over `bytes` (< 2^31) from base: dwords past them read as zero.
+__device__ __forceinline__ u32x4 buffer_load16_within(const void* base, uint32_t bytes, uint32_t voff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_raw_buffer_load_b128(
+      __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00020000), voff, 0, 0);
+#else
+  return u32x4{0u, 0u, 0u, 0u};
+#endif
+}
+
 __device__ __forceinline__ u32x2 buffer_load8(const void* base, uint32_t voff) {
 #if defined(__HIP_DEVICE_COMPILE__)
   return __builtin_amdgcn_raw_buffer_load_b64(__builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, -1, 0x00020000),

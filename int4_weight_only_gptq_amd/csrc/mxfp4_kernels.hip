@@ -149,14 +149,56 @@ __device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-// Scale bytes kb .. kb + 3 of a row of `blocks` blocks, one each past the end.
-__device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int kb, int blocks, bool dwords) {
-  if (dwords && kb + 4 <= blocks) return *reinterpret_cast<const uint32_t*>(row + kb);
-  uint32_t s = kOneScales;
+// The bytes of a scale matrix, first to one past the last row's last.
+struct Bytes {
+  const uint8_t *first, *end;
+};
+
+// Scales of one in place of those past the end of k (blocks kb ..).
+template <int D>
+__device__ __forceinline__ void ones_past_end(int kb, int blocks, uint32_t (&s)[D]) {
+  if (kb + 4 * D <= blocks) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (kb + i < blocks) s = (s & ~(0xFFu << (8 * i))) | ((uint32_t)row[kb + i] << (8 * i));
-  return s;
+  for (int i = 0; i < D; ++i) {
+    const int n = blocks - kb - 4 * i;             // valid bytes of dword i
+    const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - 8 * n);
+    s[i] = (s[i] & keep) | (kOneScales & ~keep);
+  }
+}
+
+// 4 D scale bytes from block kb on of a row of `blocks` blocks, ones past its end.  Rows
+// may start on any byte: the D + 1 aligned dwords around them are loaded and shifted
+// where those lie inside the matrix (K = 5152, rows of 161 bytes, 512 x 5120: 41.0 us byte by
+// byte, 22.6 us so).
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* row, int kb, int blocks, Bytes all, uint32_t (&s)[D]) {
+  const uint8_t* p = row + kb;
+  const uint32_t shift = (uint32_t)(uintptr_t)p & 3u;
+  const uint8_t* a = p - shift;
+  if (a >= all.first && a + 4 * D + 4 <= all.end) {
+    uint32_t w[D + 1];
+#pragma unroll
+    for (int i = 0; i <= D; ++i) w[i] = reinterpret_cast<const uint32_t*>(a)[i];
+#pragma unroll
+    for (int i = 0; i < D; ++i) s[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], shift);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      s[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (kb + 4 * i + j < blocks) s[i] |= (uint32_t)p[4 * i + j] << (8 * j);
+    }
+  }
+  ones_past_end<D>(kb, blocks, s);
+}
+
+// One dword of them; dwords: the rows start on 4 bytes.
+__device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int kb, int blocks, bool dwords, Bytes all) {
+  if (dwords && kb + 4 <= blocks) return *reinterpret_cast<const uint32_t*>(row + kb);
+  uint32_t s[1];
+  load_scales<1>(row, kb, blocks, all, s);
+  return s[0];
 }
 
 template <int RT, int DTYPE>
@@ -169,6 +211,7 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
   const int r = lane & 15, q = lane >> 4;
   const int64_t r0 = (int64_t)tm * ROWS, n0 = (int64_t)tn * 16;
   const int blocks = (int)(g.K >> 5);
+  const Bytes a_all = {g.as, g.as + (g.M - 1) * g.ldas + blocks}, b_all = {g.bs, g.bs + (g.N - 1) * g.ldbs + blocks};
   const int64_t bn = min(n0 + r, g.N - 1);
   const uint8_t *bp = g.b + bn * g.ldb, *bs = g.bs + bn * g.ldbs;
   const uint8_t *ap[RT], *as[RT];
@@ -188,7 +231,7 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
     if (16 * c + 16 <= blocks) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) b[s] = *reinterpret_cast<const u32x4*>(bp + 16 * (kb + s));
-      sb = load_scales4(bs, kb, blocks, b_dwords);
+      sb = load_scales4(bs, kb, blocks, b_dwords, b_all);
 #pragma unroll
       for (int f = 0; f < RT; ++f) {
 #pragma unroll
@@ -197,7 +240,7 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
         if (r0 + 16 * f + r < g.M) {
 #pragma unroll
           for (int s = 0; s < 4; ++s) a[f][s] = *reinterpret_cast<const u32x4*>(ap[f] + 16 * (kb + s));
-          sa[f] = load_scales4(as[f], kb, blocks, a_dwords);
+          sa[f] = load_scales4(as[f], kb, blocks, a_dwords, a_all);
         }
       }
     } else {   // past the end of k: codes of zero, scales of one
@@ -212,9 +255,9 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
           if (!in) a[f][s] = u32x4{0u, 0u, 0u, 0u};
         }
       }
-      sb = load_scales4(bs, kb, blocks, b_dwords);
+      sb = load_scales4(bs, kb, blocks, b_dwords, b_all);
 #pragma unroll
-      for (int f = 0; f < RT; ++f) sa[f] = load_scales4(as[f], kb, blocks, a_dwords);
+      for (int f = 0; f < RT; ++f) sa[f] = load_scales4(as[f], kb, blocks, a_dwords, a_all);
     }
 #pragma unroll
     for (int f = 0; f < RT; ++f) {
@@ -264,16 +307,6 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
 // ---------------------------------------------------------------------------
 constexpr int kMxBand = 8;   // row tiles per band of the tile order
 
-// The 16 scale bytes from block kb on of a row, ones past its end.  align: the rows'
-// alignment in bytes (16, 4 or 1).
-__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int kb, int blocks, int align) {
-  if (align == 16 && kb + 16 <= blocks) return *reinterpret_cast<const u32x4*>(row + kb);
-  u32x4 s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = load_scales4(row, kb + 4 * i, blocks, align >= 4);
-  return s;
-}
-
 template <int BM, int BN, int KB, int STAGES>
 struct MxTile {
   static constexpr int kStage = (BM + BN) * KB;                 // 16-byte chunks
@@ -284,14 +317,13 @@ struct MxTile {
   }
 };
 
-template <int BM, int BN, int KB, int STAGES, int NWV, int WGM, int DTYPE>
+template <int BM, int BN, int KB, int STAGES, int NWV, int WGM, int DTYPE, bool ALIGN16>
 __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int tiles_m, int tiles_n, int per_xcd,
-                                                              int a_align, int b_align, int vec) {
+                                                              int vec) {
   constexpr int T = 64 * NWV, WM = BM / WGM, WN = BN / (NWV / WGM), FM = WM / 32, FN = WN / 32;
   constexpr int STEPS = KB / 2, PER = 16 / KB;                   // steps of a k tile; k tiles of a scale buffer
   using S = MxTile<BM, BN, KB, STAGES>;
   constexpr int LOADS = S::kStage / T, A_LOADS = BM * KB / T;
-  constexpr int SROWS = (BM + BN + T - 1) / T;                   // rows of scales a thread stages
   static_assert((KB == 4 || KB == 8) && BM * KB % T == 0 && BN * KB % T == 0 && LOADS * (STAGES - 1) <= 63, "loads");
   extern __shared__ __attribute__((aligned(16))) u32x4 msm[];
   uint32_t* ssm = reinterpret_cast<uint32_t*>(msm + STAGES * S::kStage);   // scales [2][4][BM + BN]
@@ -330,26 +362,34 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
       buffer_to_lds16_or_zero((j < A_LOADS ? abase : bbase) + (int64_t)kt * 16 * KB, in ? off[j] : kOutside,
                               base + T * j);
   };
-  // rows tid + T i of scales, A's then B's
-  const uint8_t* sp[SROWS];
-#pragma unroll
-  for (int i = 0; i < SROWS; ++i) {
-    const int row = tid + T * i;
-    sp[i] = row < BM ? g.as + min(m0 + row, g.M - 1) * g.ldas : g.bs + min(n0 + row - BM, g.N - 1) * g.ldbs;
-  }
-  u32x4 staged[SROWS];
-  auto load_scales = [&](int kb) {
-#pragma unroll
-    for (int i = 0; i < SROWS; ++i)
-      if (tid + T * i < BM + BN) staged[i] = load_scales16(sp[i], kb, blocks, tid + T * i < BM ? a_align : b_align);
+  // Row tid of scales, A's then B's (a wave holds rows of one of them), 16 blocks at a time.
+  // ALIGN16: every row starts on 16 bytes; a variant of its own, because the general form takes
+  // registers that the largest tile has not (9 spilled, 2048 x 8192 at k = 8192 72 -> 80 us).
+  // Its load ends with the dword that holds the matrix's last byte.
+  static_assert(BM % 64 == 0 && BM + BN <= T, "rows of scales");
+  const bool mine = tid < BM + BN, of_a = 64 * wave < BM;
+  const uint8_t* sfirst = of_a ? g.as + m0 * g.ldas : g.bs + n0 * g.ldbs;
+  const int64_t sld = of_a ? g.ldas : g.ldbs, srows = of_a ? g.M - m0 : g.N - n0;
+  const uint32_t soff = (uint32_t)min((int64_t)(of_a ? tid : tid - BM), srows - 1) * (uint32_t)sld;
+  const int64_t sbytes = (srows - 1) * sld + blocks;
+  const uint32_t srange = (uint32_t)min((sbytes + 3) & ~(int64_t)3, (int64_t)kOutside - 4);
+  u32x4 staged;
+  auto stage_scales = [&](int kb) {
+    if (!mine) return;
+    uint32_t s[4];
+    if constexpr (ALIGN16) {
+      const u32x4 v = buffer_load16_within(sfirst, srange, soff + kb);
+      s[0] = v[0]; s[1] = v[1]; s[2] = v[2]; s[3] = v[3];
+      ones_past_end<4>(kb, blocks, s);
+    } else {
+      load_scales<4>(sfirst + soff, kb, blocks, Bytes{of_a ? g.as : g.bs, sfirst + sbytes}, s);
+    }
+    staged = u32x4{s[0], s[1], s[2], s[3]};
   };
   auto store_scales = [&](int buf) {
+    if (!mine) return;
 #pragma unroll
-    for (int i = 0; i < SROWS; ++i)
-      if (tid + T * i < BM + BN) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ssm[(4 * buf + j) * S::kScales + tid + T * i] = staged[i][j];
-      }
+    for (int j = 0; j < 4; ++j) ssm[(4 * buf + j) * S::kScales + tid] = staged[j];
   };
 
   f32x16 acc[FM][FN];
@@ -398,7 +438,7 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
 #pragma unroll
   for (int st = 0; st < STAGES; ++st)
     if (st < ktiles) issue(st);
-  load_scales(0);
+  stage_scales(0);
   store_scales(0);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -408,7 +448,7 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
   read_scales(0, sc);
   // one k tile; refill = kt + STAGES < ktiles, next = kt + 1 < ktiles (compile time)
   auto tile = [&](int kt, auto refill, auto next) {
-    if (kt % PER == 0 && kt + PER < ktiles) load_scales(KB * (kt + PER));
+    if (kt % PER == 0 && kt + PER < ktiles) stage_scales(KB * (kt + PER));
     auto step = [&](auto s_) {
       constexpr int s = decltype(s_)::value;
       read(kt, s + 1, x[(s + 1) & 1]);
@@ -534,6 +574,44 @@ struct MxPlan {
   int64_t tiles_m, tiles_n;
 };
 
+constexpr int kCus = 256;
+
+// Tiles of the many-row kernel, one workgroup a CU: a launch takes ceil(tiles / 256) rounds
+// of one tile's time.  Measured per round against 256 x 256 (bf16, k = 5120, 35 us): 128 x 128
+// half of it, 64 x 128 0.36.  512 x 5120 17.2 us with 128 x 128 against 23.6 (64) and 36.8 (256),
+// 2000 x 1024 13.4 us with 64 x 128 against 18.0 (128), 2048 x 8192 at k = 8192 72 us with
+// 256 x 256 against 108 (128).
+struct MxTileSize {
+  int bm, bn, threads;
+  double cost;
+};
+static const MxTileSize kMxTiles[3] = {{256, 256, 512, 1.0}, {128, 128, 256, 0.5}, {64, 128, 256, 0.36}};
+
+static double tile_cost(const MxTileSize& t, int64_t M, int64_t N) {
+  const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+  return (double)((tiles + kCus - 1) / kCus) * t.cost;
+}
+
+static const MxTileSize& pick_tile(int64_t M, int64_t N) {
+  const MxTileSize* best = &kMxTiles[0];
+  for (const MxTileSize& t : kMxTiles)
+    if (tile_cost(t, M, N) < tile_cost(*best, M, N)) best = &t;
+  return *best;
+}
+
+// Columns of a first launch of whole rounds of 256 x 256 tiles when the columns that are
+// left are cheaper in tiles of their own, a second launch being charged a tenth of a
+// round; 0: one launch.  (2000 x 25600, 800 tiles: 24576 columns in three rounds and 1024 in one
+// of 64 x 128 tiles, 173 -> FFF us.)
+static int64_t first_columns(int64_t M, int64_t N) {
+  const double one = tile_cost(pick_tile(M, N), M, N);
+  const int64_t tiles_m = (M + 255) / 256, rounds = tiles_m * ((N + 255) / 256) / kCus;
+  const int64_t n1 = rounds * kCus / tiles_m * 256;
+  if (rounds == 0 || n1 <= 0 || n1 >= N) return 0;
+  const double two = tile_cost(kMxTiles[0], M, n1) + tile_cost(pick_tile(M, N - n1), M, N - n1) + 0.1;
+  return two < one ? n1 : 0;
+}
+
 static MxPlan plan_mxfp4(const MxGemmArgs& g) {
   MxPlan p{};
   if (g.M <= 32 || g.K == 0) {
@@ -543,10 +621,10 @@ static MxPlan plan_mxfp4(const MxGemmArgs& g) {
     const int64_t chunks = (g.K + 511) / 512;
     p.threads = (int)(64 * (chunks < 1 ? 1 : chunks < 8 ? chunks : 8));
   } else {
-    const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    p.bm = p.bn = big >= 200 ? 256 : 128;
-    if (g.M <= 64) p.bm = 64, p.bn = 128;
-    p.threads = p.bm == 256 ? 512 : 256;
+    const MxTileSize& t = pick_tile(g.M, g.N);
+    p.bm = t.bm;
+    p.bn = t.bn;
+    p.threads = t.threads;
   }
   p.tiles_m = (g.M + p.bm - 1) / p.bm;
   p.tiles_n = (g.N + p.bn - 1) / p.bn;
@@ -565,8 +643,12 @@ static void mx_tile_launch(const MxGemmArgs& g, const MxPlan& p, hipStream_t str
   static_assert(lds <= 160 * 1024, "LDS budget");
   const int per_xcd = (int)((p.tiles_m * p.tiles_n + 7) / 8);
   const int vec = row_align(g.c, g.ldc * 2) == 16;
-  mxfp4_tile_kernel<BM, BN, KB, STAGES, NWV, WGM, DTYPE><<<dim3((unsigned)(8 * per_xcd)), dim3(64 * NWV), lds, stream>>>(
-      g, (int)p.tiles_m, (int)p.tiles_n, per_xcd, row_align(g.as, g.ldas), row_align(g.bs, g.ldbs), vec);
+  const dim3 grid((unsigned)(8 * per_xcd)), block(64 * NWV);
+  const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
+  if (row_align(g.as, g.ldas) == 16 && row_align(g.bs, g.ldbs) == 16)
+    mxfp4_tile_kernel<BM, BN, KB, STAGES, NWV, WGM, DTYPE, true><<<grid, block, lds, stream>>>(g, tm, tn, per_xcd, vec);
+  else
+    mxfp4_tile_kernel<BM, BN, KB, STAGES, NWV, WGM, DTYPE, false><<<grid, block, lds, stream>>>(g, tm, tn, per_xcd, vec);
 }
 
 template <int DTYPE>
@@ -588,6 +670,17 @@ static void mx_dispatch(const MxGemmArgs& g, hipStream_t stream) {
 }
 
 hipError_t launch_mxfp4_gemm(int dtype, const MxGemmArgs& g, hipStream_t stream) {
+  const int64_t n1 = g.M > 32 && g.K > 0 ? first_columns(g.M, g.N) : 0;
+  if (n1 > 0) {
+    MxGemmArgs lo = g, hi = g;
+    lo.N = n1;
+    hi.N = g.N - n1;
+    hi.b = g.b + n1 * g.ldb;
+    hi.bs = g.bs + n1 * g.ldbs;
+    hi.c = static_cast<char*>(g.c) + n1 * (dtype == 2 ? 4 : 2);
+    const hipError_t e = launch_mxfp4_gemm(dtype, lo, stream);
+    return e != hipSuccess ? e : launch_mxfp4_gemm(dtype, hi, stream);
+  }
   if (dtype == 0) mx_dispatch<0>(g, stream);
   else if (dtype == 1) mx_dispatch<1>(g, stream);
   else mx_dispatch<2>(g, stream);
