@@ -53,7 +53,7 @@ struct GroupTiles {
   __device__ __forceinline__ GroupTiles(const int32_t* offsets_, int groups_, int rows_, int bm_, int tiles_n_,
                                         int band_, int lane_)
       : offsets(offsets_), groups(groups_), rows(rows_), bm(bm_), tiles_n(tiles_n_), band(band_), lane(lane_) {
-    int row_tiles = 0;
+    int64_t row_tiles = 0;
     for (int c = 0; c < groups; c += 64) {
       int lo, r, sum;
       chunk(c, lo, r, sum);
@@ -64,7 +64,9 @@ struct GroupTiles {
       }
       row_tiles += __builtin_amdgcn_readlane(sum, 63);
     }
-    tiles = (int64_t)row_tiles * tiles_n;
+    // (offsets in order never give more; others, whose groups may overlap, stop here)
+    if (row_tiles > rows / bm + groups) row_tiles = rows / bm + groups;
+    tiles = row_tiles * tiles_n;
   }
 
   // groups c .. c + 63, one a lane: first row, rows, inclusive sum of row tiles
@@ -88,8 +90,8 @@ struct GroupTiles {
     GroupTile g{-1, 0, 0, 0, 0};
     const int64_t per_xcd = (tiles + 7) >> 3, item = x * per_xcd + i;
     if (i >= per_xcd || item >= tiles) return g;
-    const int q = (int)(item / tiles_n);   // row tiles before it, over all groups
-    int base = 0;
+    const uint32_t q = (uint32_t)(item / tiles_n);   // row tiles before it, over all groups (below 2^31)
+    uint32_t base = 0;
     for (int c = 0; c < groups; c += 64) {
       int lo = lo0, r = rows0, sum = sum0;
       if (c > 0) chunk(c, lo, r, sum);
@@ -100,7 +102,7 @@ struct GroupTiles {
         g.row0 = __builtin_amdgcn_readlane(lo, l);
         g.rows = __builtin_amdgcn_readlane(r, l);
         const int rt = (g.rows + bm - 1) / bm;
-        const int start = base + __builtin_amdgcn_readlane(sum, l) - rt;
+        const int start = (int)base + __builtin_amdgcn_readlane(sum, l) - rt;
         const int local = (int)(item - (int64_t)start * tiles_n);
         const int b = local / (band * tiles_n), in = local - b * band * tiles_n;
         const int height = min(band, rt - b * band);

@@ -35,6 +35,7 @@ CONVERT = [
     (dict(ldx=63), SHAPE), (dict(ldc=16), SHAPE), (dict(lds=1), SHAPE),
     (dict(x=A16 + 1), ALIGN), (dict(dtype=2, x=A16 + 2), ALIGN), (dict(codes=A16 + 8), ALIGN), (dict(ldc=40), ALIGN),
     (dict(rows=1 << 31, k=32, ldx=32, ldc=16), SHAPE),
+    (dict(ldc=(1 << 22) + 16), SHAPE), (dict(lds=(1 << 22) + 1), SHAPE),
     (dict(rows=0, x=0, codes=0, scales=0), OK), (dict(k=0, x=0, codes=0, scales=0), OK),
 ]
 
@@ -55,6 +56,8 @@ def test_quantize_and_dequantize_reject_invalid_arguments(lib, kw, code):
     (dict(c=0), NULL), (dict(lda=16), SHAPE), (dict(lsa=1), SHAPE), (dict(ldb=16), SHAPE), (dict(lsb=1), SHAPE),
     (dict(ldc=7), SHAPE), (dict(a=A16 + 8), ALIGN), (dict(ldb=40), ALIGN), (dict(c=A16 + 1), ALIGN),
     (dict(dtype=2, c=A16 + 2), ALIGN), (dict(M=1 << 30, N=1 << 30, ldc=1 << 30), SHAPE),
+    (dict(lda=(1 << 22) + 16), SHAPE), (dict(ldb=(1 << 22) + 16), SHAPE),
+    (dict(lsa=(1 << 22) + 1), SHAPE), (dict(lsb=(1 << 22) + 1), SHAPE),
     (dict(M=0, a=0, sa=0, b=0, sb=0, c=0), OK), (dict(N=0, a=0, sa=0, b=0, sb=0, c=0), OK),
 ])
 def test_gemm_mxfp4_rejects_invalid_arguments(lib, kw, code):

@@ -107,8 +107,8 @@ def test_small_shapes(gpu_lib, layout, dtype):
             assert_close(run(gpu_lib, layout, a, b, off), layout, dtype, a, b, off, (counts, N, K))
 
 
-# averages that reach every kernel: strips of 16 and 32 rows, pipelined tiles of 64, 128
-# and 256 rows; k with a tail and a k longer than the strips' waves
+# averages that reach every kernel: strips of 16 rows, pipelined tiles of 64, 128 and 256
+# rows; k with a tail and a k longer than the strips' waves
 AVERAGES = [([1, 3, 0, 12], 5), ([20, 0, 47, 9], 1), ([64, 40, 0, 90], 1), ([100, 200, 1, 99], 1), ([500, 0, 129], 1),
             ([300, 700, 0, 1400], 1)]
 
@@ -131,6 +131,58 @@ def test_many_groups(gpu_lib, groups):
         say("groups", groups, layout, sum(counts))
         a, b, off = make(layout, "bf16", counts, N, K, seed=groups)
         assert_close(run(gpu_lib, layout, a, b, off), layout, "bf16", a, b, off, (groups, layout))
+
+
+# more groups than a wave has lanes, in strips, in tiles of 64 and 256 rows and (TN) in tiles
+# of 256 x 256 and 128 x 256; a workgroup takes several tiles
+@pytest.mark.parametrize("layout,groups,most,N,K", [("NT", 70, 3, 384, 264), ("NN", 70, 3, 384, 264),
+                                                    ("NT", 130, 200, 264, 72), ("NN", 130, 200, 264, 72),
+                                                    ("NT", 67, 700, 512, 40), ("NN", 67, 700, 512, 40),
+                                                    ("TN", 150, 90, 264, 136), ("TN", 70, 60, 512, 512),
+                                                    ("TN", 100, 40, 128, 256)])
+def test_many_groups_of_many_rows(gpu_lib, layout, groups, most, N, K):
+    rng = np.random.default_rng(groups + most)
+    counts = (rng.integers(0, most, groups) * (rng.random(groups) < 0.8)).tolist()
+    for dtype in ("bf16", "fp16"):
+        say("many", layout, groups, sum(counts), N, K, dtype)
+        a, b, off = make(layout, dtype, counts, N, K, seed=groups)
+        assert_close(run(gpu_lib, layout, a, b, off), layout, dtype, a, b, off, (layout, groups))
+
+
+@pytest.mark.parametrize("layout", ["NT", "TN"])
+@pytest.mark.parametrize("ld", [2 ** 21, 2 ** 21 + 8])
+def test_rows_past_32_bits(gpu_lib, layout, ld):
+    """Rows whose byte offsets pass 32 bits, at the widest leading dimension of the pipelined
+    kernel and past it."""
+    import torch
+
+    counts, N, K = [700, 0, 340, 60], 72, 64
+    a, b, off = make(layout, "bf16", counts, N, K, seed=21)
+    wide = torch.empty((a.shape[0], ld), dtype=torch.bfloat16, device="cuda")
+    wide[:, :a.shape[1]] = a.cuda()
+    out = None
+    if layout == "NT":
+        out = torch.empty((a.shape[0], ld), dtype=torch.bfloat16, device="cuda")[:, 8:8 + N]
+    got = gpu_lib.gemm_grouped(layout, wide[:, :a.shape[1]], b.cuda(), off.cuda(), out=out)
+    torch.cuda.synchronize()
+    assert_close(got, layout, "bf16", a, b, off, (layout, ld))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["NT", "NN", "TN"])
+def test_overlapping_groups_end(gpu_lib, layout, dtype):
+    """Offsets that go back and forth (groups that overlap) are not a product's, but the call
+    ends and writes nothing outside the output; the next call is right."""
+    import torch
+
+    a, b, off = make(layout, dtype, [4] * 200, 72, 64, seed=25)
+    shape = (200, 72, 64) if layout == "TN" else (800, 72)
+    hold = torch.full((shape[0] + 64,) + shape[1:], 7.0, dtype=tdtype(dtype), device="cuda")
+    wild = torch.tensor([0, 800] * 100 + [0], dtype=torch.int32)
+    gpu_lib.gemm_grouped(layout, a.cuda(), b.cuda(), wild.cuda(), out=hold[32:-32])
+    torch.cuda.synchronize()
+    assert torch.all(hold[:32] == 7.0) and torch.all(hold[-32:] == 7.0)
+    assert_close(run(gpu_lib, layout, a, b, off), layout, dtype, a, b, off, (layout, dtype))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])

@@ -103,6 +103,30 @@ def test_wide_strips(gpu_lib):
             assert_close(run(gpu_lib, d), d, (experts, n, most))
 
 
+@pytest.mark.parametrize("experts,most", [(70, 3), (130, 30), (100, 90), (66, 300), (65, 700)])
+def test_more_experts_than_lanes(gpu_lib, experts, most):
+    rng = np.random.default_rng(experts)
+    counts = (rng.integers(0, most, experts) * (rng.random(experts) < 0.8)).tolist()
+    say("int4 experts", experts, sum(counts))
+    d = make(counts, 136, 256, seed=experts)
+    for workspace in (None, False):
+        assert_close(run(gpu_lib, d, workspace=workspace), d, (experts, most, workspace))
+
+
+@pytest.mark.parametrize("most", [2, 20, 100])
+def test_overlapping_experts_end(gpu_lib, most):
+    """Offsets that go back and forth end, and write nothing outside the output."""
+    import torch
+
+    d = make([most] * 80, 72, 256, seed=13)
+    rows = 80 * most
+    hold = torch.full((rows + 64, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+    wild = {**d, "offsets": torch.tensor([0, rows] * 40 + [0], dtype=torch.int32)}
+    run(gpu_lib, wild, out=hold[32:-32])
+    assert torch.all(hold[:32] == 7.0) and torch.all(hold[-32:] == 7.0)
+    assert_close(run(gpu_lib, d), d, most)
+
+
 @pytest.mark.parametrize("counts", [[2, 0, 3], [50, 0, 40], [180, 0, 90]])
 def test_rows_of_no_expert_stay(gpu_lib, counts):
     import torch

@@ -223,6 +223,48 @@ def test_large_tiles(gpu_lib, K):
         assert_product(part, (a[0][rows], a[1][rows]), (b[0][cols], b[1][cols]), dtype, (dtype, K))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,N", [(1500, 12000), (2000, 9300)])
+def test_columns_past_whole_rounds(gpu_lib, dtype, M, N):
+    """More 256 x 256 tiles than CUs and few in the last round: a second launch takes the columns
+    that are left (from 10752 and 8192 on).  The scales' rows start on any byte; the output is a
+    view that starts on any element."""
+    import torch
+
+    say("mxfp4 columns", dtype, M, N)
+    K = 288
+    spread = 2 if dtype == "fp16" else 8
+    a, b = mx_matrix(M, K, 3, spread), mx_matrix(N, K, 4, spread)
+    hold = torch.full((M + 1, N + 5), 7.0, dtype=tdtype(dtype), device="cuda")
+    out = gpu_lib.gemm_mxfp4(*up(a), *up(b), out=hold[:M, 3:3 + N])
+    torch.cuda.synchronize()
+    rows = np.unique(np.concatenate([np.arange(0, M, 61), [255, 256, M - 1]]))
+    cols = np.unique(np.concatenate([np.arange(0, N, 53), [8191, 8192, min(10751, N - 2), min(10752, N - 2), N - 1]]))
+    part = out[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()]
+    assert_product(part, (a[0][rows], a[1][rows]), (b[0][cols], b[1][cols]), dtype, (dtype, M, N))
+    hold[:M, 3:3 + N] = 7.0
+    assert torch.all(hold == 7.0)
+
+
+@pytest.mark.parametrize("M", [8, 24, 700])
+def test_rows_past_32_bits(gpu_lib, M):
+    """The widest leading dimensions: offsets of codes, scales and results past 32 bits."""
+    import torch
+
+    K, N, ld = 544, 600, 2 ** 22
+    a, b = mx_matrix(M, K, 1), mx_matrix(N, K, 2)
+
+    def wide(m):
+        hold = torch.empty((m.shape[0], ld), dtype=torch.uint8, device="cuda")
+        hold[:, :m.shape[1]] = torch.from_numpy(m).cuda()
+        return hold[:, :m.shape[1]]
+
+    out = torch.empty((M, 2 ** 22), dtype=torch.bfloat16, device="cuda")[:, :N]
+    gpu_lib.gemm_mxfp4(wide(a[0]), wide(a[1]), wide(b[0]), wide(b[1]), out=out)
+    torch.cuda.synchronize()
+    assert_product(out, a, b, "bf16", M)
+
+
 def test_scales_of_every_alignment_and_padding(gpu_lib):
     """Scale rows on 16, 4 and 1 bytes give the same bits; padding behind rows (NaN scales, any
     codes) is never used."""
