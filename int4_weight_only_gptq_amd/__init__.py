@@ -465,6 +465,8 @@ def _device_of(first, *others):
 
 def _rows_ld(t, what):
     """Distance in elements between the rows of a matrix, or of each matrix of a stack."""
+    if t.is_contiguous():
+        return t.shape[-1]
     st, sh = t.stride(), t.shape
     if st[-1] != 1 and sh[-1] > 1 and t.numel():
         raise ValueError("the last dimension of %s must be contiguous" % what)
@@ -572,6 +574,8 @@ def _int4_grouped(x, qweight, scales, qzeros, offsets, out, group_size, workspac
         if size < 0:
             raise QGemmError(-size, "qgemm_int4_grouped_workspace_size")
         workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else False
+    elif workspace is not False and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     wptr, wbytes = ((None, 0) if workspace is False
                     else (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     st = lib.qgemm_int4_grouped(x.data_ptr(), _rows_ld(x, "x"), qweight.data_ptr(), scales.data_ptr(),

@@ -214,5 +214,7 @@ def test_refusals(gpu_lib):
             f(*bad)
     with pytest.raises(gpu_lib.QGemmError):
         f(x, qw, sc, qz, off, group_size=64)
+    with pytest.raises(ValueError):
+        f(x, qw, sc, qz, off, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")[::2])
     with pytest.raises(gpu_lib.QGemmError):
         f(x, qw, sc, qz, off, workspace=torch.empty(33, dtype=torch.uint8, device="cuda")[1:])
