@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
 
   // chunk tid + T j of a stage: row (tid + T j) / KB of the tile's A rows then B rows
   // (rows past M or N repeat the last one), its k chunk the same for every j
-  auto swizzle = [](int row, int c) { return KB == 8 ? c ^ (row & 7) : c ^ ((row >> 2) & 3); };
+  auto swizzle = [](int row, int c) { return KB == 8 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3); };
   static_assert(T / KB % 16 == 0, "one k chunk per thread");
   const int chunk = swizzle(tid / KB, tid % KB);
   const uint8_t *abase = g.a + m0 * g.lda, *bbase = g.b + n0 * g.ldb;
@@ -661,7 +661,7 @@ static void mx_dispatch(const MxGemmArgs& g, hipStream_t stream) {
     if (p.bm == 16) mxfp4_strip_kernel<1, DTYPE><<<grid, block, lds, stream>>>(g, (int)p.tiles_n, ad, bd);
     else mxfp4_strip_kernel<2, DTYPE><<<grid, block, lds, stream>>>(g, (int)p.tiles_n, ad, bd);
   } else if (p.bm == 256) {
-    mx_tile_launch<256, 256, 8, 2, 8, 4, DTYPE>(g, p, stream);
+    mx_tile_launch<256, 256, 8, 2, 8, 2, DTYPE>(g, p, stream);
   } else if (p.bm == 128) {
     mx_tile_launch<128, 128, 8, 4, 4, 2, DTYPE>(g, p, stream);
   } else {
