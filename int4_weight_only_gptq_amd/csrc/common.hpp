@@ -312,11 +312,12 @@ __device__ __forceinline__ void buffer_to_lds16_or_zero(const void* base, uint32
 
 // 16 bytes per lane stored through the same kind of resource: lanes whose offset is
 // kOutside store nothing.  Every lane takes part, so the number of stores a wave has
-// in flight is known.
+// in flight is known.  Non-temporal: results do not push the operands out of L2 (weight
+// gradients of 8192 rows over 32 groups, 2048 x 5632: 311 -> 261 us).
 __device__ __forceinline__ void buffer_store16_or_none(void* base, uint32_t voff, u32x4 v) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_raw_buffer_store_b128(
-      v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)kOutside, 0x00020000), voff, 0, 0);
+      v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)kOutside, 0x00020000), voff, 0, 2);
 #endif
 }
 

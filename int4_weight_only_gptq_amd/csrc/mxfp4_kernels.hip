@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t* __
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = DTYPE == 0 ? pack_bf16x2(v[2 * j], v[2 * j + 1]) : pack_f16x2(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<u32x4*>(p) = o;
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));    // (4096 x 14336 and its quantisation 48.5 -> 45.8 us)
   }
 }
 
@@ -519,7 +519,8 @@ __global__ __launch_bounds__(64 * NWV) void mxfp4_tile_kernel(MxGemmArgs g, int 
       if (gr >= g.M || gc >= g.N) continue;
       const uint16_t* p = &osm[row * OP + 8 * cc];
       if (vec && gc + 8 <= g.N) {
-        *reinterpret_cast<u32x4*>(out + gr * g.ldc + gc) = *reinterpret_cast<const u32x4*>(p);
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(p),
+                                    reinterpret_cast<u32x4*>(out + gr * g.ldc + gc));
       } else {
         for (int e = 0; e < 8 && gc + e < g.N; ++e) out[gr * g.ldc + gc + e] = p[e];
       }
