@@ -6,8 +6,8 @@
 // bf16 / fp16 with fp32 accumulation, or fp32 throughout.  Three kernels:
 //  * many rows a group: pipelined MFMA tiles, a workgroup on each CU going from tile
 //    to tile;
-//  * few rows in few groups (decoding), where the tiles would not reach every CU: a
-//    workgroup takes a strip of columns over the whole of k, split over its waves;
+//  * few rows a group (decoding): a workgroup takes a strip of columns over the whole of
+//    k, split over its waves;
 //  * any alignment and size, and fp32: a tile staged through registers.
 #include "common.hpp"
 #include "groups.hpp"
@@ -365,22 +365,23 @@ __global__ __launch_bounds__(64 * NWV) void grouped_pipe_kernel(GroupedArgs a, i
 // ---------------------------------------------------------------------------
 // few rows a group: strips of columns over the whole of k
 //
-// Where the tiles would reach fewer than the 256 CUs.  A workgroup owns 16 rows of a group
-// and a strip of columns; its waves take
-// blocks of k in turn, all loads of a block issued before its MFMAs, operands
-// straight from memory into the MFMA lane layout (lane l: row or column l % 16, k
-// chunk l / 16), and the waves' partial tiles are summed through LDS in wave
-// order.  The activations are read from L2, only by the lanes whose rows there are.
+// A workgroup owns 16 rows of a group and a strip of columns; its waves take blocks of
+// k in turn, all loads of a block issued before its MFMAs, operands straight from memory
+// into the MFMA lane layout (lane l: row or column l % 16, k chunk l / 16), and the waves'
+// partial tiles are summed through LDS in wave order.  The activations are read from L2,
+// only by the lanes whose rows there are.
 // ---------------------------------------------------------------------------
 // NT, B K-contiguous: strip of 16 columns, blocks of 256 k, so a column's 512
 // contiguous bytes are read by one wave.
 // NN, B N-contiguous: strip of 128 columns; lane (c, q) loads columns 8c .. 8c + 7
 // of the 8 k-rows 8q .. 8q + 7 and transposes the 8 x 8 block in registers:
 // fragment j then holds column 8c + j (256 contiguous bytes per k-row).
-// With enough tiles the pipelined kernel streams the weights as fast (64 rows over 64 experts,
-// 2048 -> 1024, bf16 NT 31.4 us here, 32.3 us there) and faster from a few rows a group on (512
-// rows 64.7 vs 43.9 us), since it does not load rows that are not there.
-constexpr int kStripRows = 8;     // rows a group at most, on average
+// Against the pipelined kernel (bf16, weights from HBM): 64 / 128 / 256 / 384 rows over 64 experts,
+// 2048 -> 1024, NT 35.6 / 47.8 / 58.4 / 64.5 us here, 47.4 / 52.4 / 58.9 / 61.6 us there; 16 / 32 / 64 rows
+// over 8, 4096 -> 8192, NT 72 / 93 / 115 against 85 / 98 / 106 us, NN 77 / 92 / 109 against 80 / 96 / 102 us: the
+// small workgroups spread evenly over the CUs, the tiles load a weight once for all rows.
+// So up to 4 rows a group on average, and up to 8 where the tiles would not reach every CU.
+constexpr int kStripRows = 4, kStripRowsFew = 8;
 constexpr int kStripK = 256;      // k per block, NT
 constexpr int kStripKN = 32;      // k per block, NN
 
@@ -704,7 +705,8 @@ static GroupedPlan plan_grouped(const GroupedArgs& a) {
       const int64_t big = a.groups * ((a.M + 255) / 256) * ((a.N + 255) / 256);
       p = big > kCus / 2 ? GroupedPlan{GroupedPlan::kPipe, 256, 256, 512, 0}
                          : GroupedPlan{GroupedPlan::kPipe, 128, 256, 256, 0};
-    } else if (avg <= kStripRows && (a.rows < a.groups ? a.rows : a.groups) * ((a.N + 127) / 128) <= kCus) {
+    } else if (avg <= kStripRows ||
+               (avg <= kStripRowsFew && (a.rows < a.groups ? a.rows : a.groups) * ((a.N + 127) / 128) <= kCus)) {
       const int64_t k_block = a.layout == 0 ? kStripK : kStripKN, waves = (a.K + k_block - 1) / k_block;
       p = {GroupedPlan::kStrip, 16, a.layout == 0 ? 16 : 128, (int)(64 * (waves < 8 ? waves : 8)), 0};
     } else {
