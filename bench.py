@@ -40,6 +40,7 @@ LLC_BYTES = 256 << 20
 # kernel sources hash to the value recorded with the counters.
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "skinny_lds_small_m_traffic.md")
 KERNEL_SOURCES = ["int4_weight_only_gptq_amd/csrc/int4_kernels.hip",
+                  "int4_weight_only_gptq_amd/csrc/int4_common.hpp",
                   "int4_weight_only_gptq_amd/csrc/common.hpp",
                   "int4_weight_only_gptq_amd/csrc/launch.hpp",
                   "int4_weight_only_gptq_amd/build.py"]
