@@ -294,7 +294,8 @@ __global__ __launch_bounds__(512) void mxfp4_strip_kernel(MxGemmArgs g, int stri
 // NWV waves as a WGM x (NWV / WGM) grid, FM x FN matrix tiles of 32 x 32 each.  k
 // tiles of KB blocks (32 KB elements, 16 KB bytes a row) in a ring of STAGES LDS
 // buffers filled by direct loads, 16-byte chunk c of row r in slot KB r + (c ^ x(r))
-// with x(r) such that the rows LDS serves together fall on different banks.  Lane
+// with x(r) such that the 16 rows LDS serves together fall on different banks (with r mod 8
+// for KB = 8 every two met: 2048 x 8192 at k = 8192 70.6 us, 67.2 with r / 2 mod 8).  Lane
 // (r, h) of 32x32x64 step s takes block h KB / 2 + s of row r, so that its scales of a
 // k tile are adjacent bytes.  Scales are staged 16 blocks (512 k) at a time, 16 bytes a
 // row, through registers into two LDS buffers of four planes (dword j of every row side
@@ -578,9 +579,9 @@ struct MxPlan {
 constexpr int kCus = 256;
 
 // Tiles of the many-row kernel, one workgroup a CU: a launch takes ceil(tiles / 256) rounds
-// of one tile's time.  Measured per round against 256 x 256 (bf16, k = 5120, 35 us): 128 x 128
+// of one tile's time.  Measured per round against 256 x 256 (bf16, k = 5120, 43 us): 128 x 128
 // half of it, 64 x 128 0.36.  512 x 5120 17.2 us with 128 x 128 against 23.6 (64) and 36.8 (256),
-// 2000 x 1024 13.4 us with 64 x 128 against 18.0 (128), 2048 x 8192 at k = 8192 72 us with
+// 2000 x 1024 12.1 us with 64 x 128 against 18.0 (128), 2048 x 8192 at k = 8192 67 us with
 // 256 x 256 against 108 (128).
 struct MxTileSize {
   int bm, bn, threads;
